@@ -23,6 +23,8 @@ MK_DEVERR_BARRIER_TIMEOUT = 0x1
 MK_DEVERR_PIPE_TIMEOUT = 0x2
 MK_DEVERR_BAD_TOKEN = 0x4
 MK_DEVERR_CAPACITY = 0x8
+MK_DEVERR_BAD_PAGE = 0x10
+MK_DEVERR_NO_PAGES = 0x20
 
 MK_DT_BF16 = 1
 MK_DT_F32 = 2
@@ -38,6 +40,8 @@ EXPORTS = [
     "mk_query_sizes", "mk_load_weights", "mk_reset_state", "mk_set_position", "mk_prefill",
     "mk_decode_step", "mk_decode_step_noalloc", "mk_verify_drafts", "mk_verify_drafts_sampled", "mk_generate", "mk_sync_status", "mk_phase_trace", "mk_launch_count",
     "mk_linear", "mk_last_error", "mk_free",
+    "mk_pages_work_ints", "mk_pages_resize", "mk_pages_fork", "mk_pages_compact", "mk_pages_copy",
+    "mk_qk_norm_rope", "mk_paged_attention", "mk_paged_attention_scratch",
 ]
 
 
@@ -93,6 +97,60 @@ class MkSizes(C.Structure):
     ]
 
 
+class MkPagedCache(C.Structure):
+    _fields_ = [
+        ("k", C.c_void_p),
+        ("v", C.c_void_p),
+        ("layer_stride", C.c_int64),
+        ("page_stride", C.c_int64),
+        ("head_stride", C.c_int64),
+        ("slot_stride", C.c_int64),
+        ("n_layers", C.c_int32),
+        ("n_pages", C.c_int32),
+        ("kv_heads", C.c_int32),
+        ("page_size", C.c_int32),
+        ("head_dim", C.c_int32),
+        ("n_seqs", C.c_int32),
+        ("max_pages", C.c_int32),
+        ("table", C.c_void_p),
+        ("len", C.c_void_p),
+        ("ref", C.c_void_p),
+        ("work", C.c_void_p),
+        ("err", C.c_void_p),
+    ]
+
+
+class MkQkRope(C.Structure):
+    _fields_ = [
+        ("dtype", C.c_int32),
+        ("rows", C.c_int32),
+        ("q_heads", C.c_int32),
+        ("kv_heads", C.c_int32),
+        ("head_dim", C.c_int32),
+        ("rot_dim", C.c_int32),
+        ("theta", C.c_double),
+        ("eps", C.c_float),
+        ("q", C.c_void_p),
+        ("ldq", C.c_int64),
+        ("k", C.c_void_p),
+        ("ldk", C.c_int64),
+        ("v", C.c_void_p),
+        ("ldv", C.c_int64),
+        ("q_gain", C.c_void_p),
+        ("k_gain", C.c_void_p),
+        ("q_out", C.c_void_p),
+        ("ldq_out", C.c_int64),
+        ("k_out", C.c_void_p),
+        ("ldk_out", C.c_int64),
+        ("positions", C.c_void_p),
+        ("cache", C.c_void_p),
+        ("layer", C.c_int32),
+        ("n", C.c_int32),
+        ("seq_start", C.c_void_p),
+        ("seqs", C.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -124,6 +182,15 @@ def load_library(path: str = LIB_PATH) -> C.CDLL:
         "mk_phase_trace": (C.c_int, [vp, vp, i32]),
         "mk_launch_count": (i64, [vp]),
         "mk_linear": (C.c_int, [vp, i64, i32, i32, vp, i64, i32, vp, i64, i32, vp, C.c_size_t, vp, vp]),
+        "mk_pages_work_ints": (i64, [vp]),
+        "mk_pages_resize": (C.c_int, [vp, vp, vp, i32, vp]),
+        "mk_pages_fork": (C.c_int, [vp, vp, vp, i32, vp]),
+        "mk_pages_compact": (C.c_int, [vp, vp]),
+        "mk_pages_copy": (C.c_int, [vp, vp, vp, vp, i32, vp]),
+        "mk_qk_norm_rope": (C.c_int, [vp, vp]),
+        "mk_paged_attention": (C.c_int, [vp, i32, vp, i64, i32, i32, vp, vp, i32, C.c_float, vp, i64, vp, C.c_size_t,
+                                         vp]),
+        "mk_paged_attention_scratch": (C.c_size_t, [vp, i32, i32]),
         "mk_last_error": (C.c_char_p, []),
         "mk_free": (None, [vp]),
     }

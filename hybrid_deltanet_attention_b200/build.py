@@ -16,8 +16,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmk.so")
-SOURCES = ["api.cu", "decode.cu", "noalloc.cu", "gemm.cu", "prefill.cu", "attn.cu"]
-HEADERS = ["mk_internal.h", "mk_model.h", "dev.cuh", "tc.cuh"]
+SOURCES = ["api.cu", "decode.cu", "noalloc.cu", "gemm.cu", "prefill.cu", "attn.cu",
+           "pages.cu", "qk_rope.cu", "paged_attn.cu"]
+HEADERS = ["mk_internal.h", "mk_model.h", "dev.cuh", "tc.cuh", "paged.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

@@ -14,6 +14,7 @@ import torch
 
 from . import _abi
 from ._abi import MkConfig, MkSizes, MkTensor, check
+from .paged import PagedCache
 
 
 def make_config(cfg, max_ctx: int, max_draft: int = 0, kv_format: int = 0) -> MkConfig:
@@ -148,6 +149,20 @@ class Model:
     @property
     def v_cache(self) -> torch.Tensor:
         return self._kv_view(self.sizes.off_v)
+
+    def kv_pages(self, page_size: int) -> "PagedCache":
+        """The model's own bf16 KV cache as a paged cache of one sequence, the model's positions (len is the
+        device position itself): for attention over it and for copying pages out of and into it, e.g. to
+        keep a prompt's keys and values in a pool. Its pages cannot be resized, forked or compacted.
+        page_size must divide max_ctx. A copied-in prefix needs S, conv_history and the position set too."""
+        c, ctx = self.shape, int(self.cfg.max_ctx)
+        if self.kv_format != _abi.MK_KV_BF16 or page_size < 1 or ctx % page_size or c.n_at < 1:
+            raise ValueError("kv_pages needs a bf16 KV cache and a page size that divides max_ctx")
+        n = ctx // page_size
+        k, v = (t.view(c.n_at, c.at_kv_heads, n, page_size, c.at_head_dim).transpose(1, 2) for t in (self.k_cache, self.v_cache))
+        dev = k.device
+        return PagedCache(k, v, torch.arange(n, dtype=torch.int32, device=dev).view(1, n), self.pos_tensor,
+                          torch.ones(n, dtype=torch.int32, device=dev), fixed=True)
 
     def kv_q8_rows(self, which: str):
         """8-bit cache rows split into (codes int8 [n_at, Hkv, max_ctx, D], scales float16

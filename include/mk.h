@@ -64,6 +64,9 @@ extern "C" {
 #define MK_DEVERR_PIPE_TIMEOUT      0x2   /* a shared-memory pipeline wait exceeded its limit */
 #define MK_DEVERR_BAD_TOKEN         0x4   /* an input token id was outside [0, vocab) */
 #define MK_DEVERR_CAPACITY          0x8   /* the device-side position reached max_ctx */
+#define MK_DEVERR_BAD_PAGE          0x10  /* paged cache: a sequence or page id out of range, an id given twice,
+                                             or a length or position that the page table cannot hold */
+#define MK_DEVERR_NO_PAGES          0x20  /* paged cache: not enough free pages */
 
 /* ---- tensor dtypes ---- */
 #define MK_DT_BF16  1     /* 2 bytes per element, bf16 bit patterns */
@@ -305,6 +308,136 @@ int64_t mk_launch_count(const mk_model* m);
 int mk_linear(const float* d_x, int64_t ldx, int32_t M, int32_t K, const void* d_w, int64_t ldw_bytes, int32_t N,
               float* d_c, int64_t ldc, int32_t accumulate, void* d_scratch, size_t scratch_bytes, int32_t* d_err,
               void* stream);
+
+/* ------------------------------------------------------------------ paged KV cache
+ * A KV cache for several sequences: its memory is cut into pages of page_size positions,
+ * and a table says which page holds which stretch of each sequence, so that sequences
+ * grow, end and share a prompt without moving anything. The operators below are building
+ * blocks beside mk_linear: they work on caller-owned device memory and need no model
+ * handle. Model caches are pages too: the state buffer's key cache of an MK_KV_BF16 model is
+ * a paged cache with layer_stride Hkv*max_ctx*D, page_stride page_size*D, head_stride
+ * max_ctx*D and slot_stride D (page_size a divisor of max_ctx), page p holding positions
+ * p*page_size and on.
+ *
+ * Position p of sequence s lies in page table[s][p / page_size], slot p % page_size. A
+ * sequence of len[s] positions uses the first ceil(len[s] / page_size) entries of its row;
+ * entries past them are -1. ref[p] counts the table entries that name page p: 0 is free.
+ * Pages that are not the last of a sequence may be shared; a partly filled page is always
+ * one sequence's own (mk_pages_fork and mk_pages_resize see to that), so appending never
+ * writes into another sequence.
+ *
+ * Key and value entry d of (layer l, page p, kv head h, slot s) lies at element
+ * l*layer_stride + p*page_stride + h*head_stride + s*slot_stride + d of k and v.
+ *
+ * Requirements (MK_ERR_ARG otherwise): head_dim 64, 128 or 256; page_size a multiple of 8, at
+ * most 65536; every stride a multiple of 8, slot_stride >= head_dim; k and v 16-byte aligned;
+ * max_pages * page_size <= 2^30. Entries of different (l, p, h, s) must not overlap.
+ *
+ * The arrays named here live on the device and are read when the call's kernels run, so a
+ * call can be captured into a CUDA graph and replayed on new lengths and tables. Calls that
+ * change a cache's pages and calls that use them are ordered by the caller (one stream, or
+ * events). Errors found on the device set a bit in *err, which stays until the caller
+ * clears it; the call concerned then changes nothing (mk_pages_resize, _fork), or leaves out
+ * what it cannot address (the others). */
+typedef struct mk_paged_cache {
+  void*    k;              /* bf16 */
+  void*    v;              /* bf16, same strides */
+  int64_t  layer_stride, page_stride, head_stride, slot_stride;   /* in elements */
+  int32_t  n_layers, n_pages, kv_heads, page_size, head_dim;
+  int32_t  n_seqs;         /* rows of the table */
+  int32_t  max_pages;      /* entries of a row */
+  int32_t* table;          /* [n_seqs][max_pages] */
+  int32_t* len;            /* [n_seqs] positions held */
+  int32_t* ref;            /* [n_pages] use counts */
+  int32_t* work;           /* [mk_pages_work_ints(cache)] scratch of the page calls */
+  int32_t* err;            /* [1] MK_DEVERR_* bits */
+} mk_paged_cache;
+
+/* int32 entries that `work` must hold for this n_pages and n_seqs (a host-side sum). */
+int64_t mk_pages_work_ints(const mk_paged_cache* c);
+
+/* Set the lengths of n different sequences (d_seqs: device int32[n], n <= n_seqs) to d_lens
+ * (device int32[n]; NULL: all 0, which frees them): pages that fall past the new end are
+ * given back, new ones taken. A partly filled page that stays at the old or new end, whichever is lower,
+ * and is shared is replaced by a copy of its used slots (positions below
+ * both lengths), so that the sequence can append. Pages are taken lowest free id
+ * first, in the order of d_seqs and of positions within a sequence, after every page
+ * given back by this call is free again, except the shared pages it replaces. With too few
+ * free pages nothing is changed (MK_DEVERR_NO_PAGES). New slots hold whatever was there. */
+int mk_pages_resize(const mk_paged_cache* c, const int32_t* d_seqs, const int32_t* d_lens, int32_t n, void* stream);
+
+/* Make sequence d_dst[i] a continuation of d_src[i] for i < n (device int32[n]): what d_dst[i]
+ * held is given back first, full pages are shared (ref + 1), and the used slots of a partly
+ * filled last page are copied to a page of its own, taken as in mk_pages_resize. A
+ * source may appear several times; destinations must differ from each other and from every
+ * source. */
+int mk_pages_fork(const mk_paged_cache* c, const int32_t* d_src, const int32_t* d_dst, int32_t n, void* stream);
+
+/* Move the used pages together: with u pages in use, the used pages with ids >= u move, in
+ * ascending order, to the free ids below u, ascending; table and ref follow. The pages
+ * left behind keep their contents. */
+int mk_pages_compact(const mk_paged_cache* c, void* stream);
+
+/* Copy whole pages, all layers and heads: page d_src[i] of `from` to page d_dst[i] of `to`,
+ * i < n (device int32[n]). The caches may be the same or differ in strides and page count
+ * (a model's own cache and a pool, for instance); n_layers, kv_heads, page_size and
+ * head_dim must agree. Destinations must differ, and with one memory no page may be
+ * both source and destination. Tables, lengths and counts are left alone. */
+int mk_pages_copy(const mk_paged_cache* from, const mk_paged_cache* to, const int32_t* d_src, const int32_t* d_dst,
+                  int32_t n, void* stream);
+
+/* Per-head norm of queries and keys and their rotation, in one pass over the projections:
+ *   x = x * gain / sqrt(mean(x^2) + eps)              (per head; skipped where the gain is NULL)
+ *   (x[i], x[i + rot_dim/2]) rotated by the angle position * theta^(-2i / rot_dim), i < rot_dim/2
+ * (half split, as the model's attention; entries from rot_dim on are only normed). Norms and
+ * rotation in fp32, angles in float64, one rounding to bf16 at the end.
+ * With `cache`: rows seq_start[i] .. seq_start[i+1]-1 are the last
+ * positions of sequence seqs[i] (or i, with seqs NULL), whose len already counts them (see
+ * mk_pages_resize): row r has position len - seq_start[i+1] + r. Keys, and the values as they
+ * are, go to `layer` of the cache in bf16. Rows outside [seq_start[0], seq_start[n]) are left as
+ * they are in q_out. A row whose position or page does not exist sets MK_DEVERR_BAD_PAGE, gets zero
+ * queries and stores nothing. Without `cache`: positions gives each row's position (any int32), and
+ * keys go to k_out. */
+typedef struct mk_qk_rope {
+  int32_t  dtype;               /* of q, k, v: MK_DT_F32 or MK_DT_BF16 */
+  int32_t  rows, q_heads, kv_heads, head_dim;   /* head_dim 64, 128 or 256 */
+  int32_t  rot_dim;             /* 0 .. head_dim, a multiple of head_dim/16 */
+  double   theta;               /* > 0 */
+  float    eps;                 /* >= 0 */
+  const void* q;  int64_t ldq;  /* [rows][q_heads][head_dim], ld = elements from row to row */
+  const void* k;  int64_t ldk;  /* [rows][kv_heads][head_dim] */
+  const void* v;  int64_t ldv;  /* with cache */
+  const void* q_gain;           /* bf16 [head_dim] or NULL */
+  const void* k_gain;
+  void*    q_out; int64_t ldq_out;   /* bf16; may be q itself when that is bf16 with the same ld */
+  void*    k_out; int64_t ldk_out;   /* bf16, without cache; may be k itself likewise */
+  const int32_t* positions;     /* device int32[rows], without cache */
+  const mk_paged_cache* cache;  /* or NULL */
+  int32_t  layer;
+  int32_t  n;                   /* sequences with new rows */
+  const int32_t* seq_start;     /* device int32[n + 1], ascending */
+  const int32_t* seqs;          /* device int32[n] or NULL */
+} mk_qk_rope;
+/* Row pitches are multiples of 8 elements and every pointer is 16-byte aligned (int32 arrays 4). */
+int mk_qk_norm_rope(const mk_qk_rope* a, void* stream);
+
+/* Causal attention of new tokens over the pages of one layer, grouped query heads:
+ *   o[r][h] = sum_{p <= pos(r)} softmax_p(scale * q[r][h] . K[p][h / (q_heads / kv_heads)]) V[p][...]
+ * Rows and positions as in mk_qk_norm_rope with a cache (the new keys are already stored);
+ * from one token per sequence to whole prompts in one call. A row that sees no position
+ * (negative position) gives zeros; rows outside [seq_start[0], seq_start[n]) are left as they
+ * are. Keys and values below a sequence's length must be finite; what lies past it, in its
+ * last page or in pages the table does not name, is never part of a result. A page id out of range sets
+ * MK_DEVERR_BAD_PAGE and reads as zeros.
+ * d_q: bf16 [rows][q_heads][head_dim], d_out: bf16 likewise, ldq / ldo elements from row to
+ * row (multiples of 8); 16-byte aligned. n <= 65536. q_heads a multiple of the cache's kv_heads.
+ * d_scratch: at least mk_paged_attention_scratch(...) bytes, 16-byte aligned; one buffer per
+ * call that may run at the same time. */
+int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const void* d_q, int64_t ldq, int32_t rows, int32_t q_heads,
+                       const int32_t* d_seq_start, const int32_t* d_seqs, int32_t n, float scale, void* d_out, int64_t ldo,
+                       void* d_scratch, size_t scratch_bytes, void* stream);
+/* Scratch for any call with at most `rows` new tokens on the current device; 0 on bad arguments. */
+size_t mk_paged_attention_scratch(const mk_paged_cache* c, int32_t rows, int32_t q_heads);
 
 /* Thread-local description of the last nonzero return on this thread. */
 const char* mk_last_error(void);
