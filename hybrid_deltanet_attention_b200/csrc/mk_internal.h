@@ -145,6 +145,10 @@ cudaError_t launch_split_bf16(const float* x, long long ldx, uint16_t* hi, uint1
 // columns x box_rows rows, 128-byte swizzle; cached per (base, shape, box).
 bool tensor_map_bf16(CUtensorMap* map, const void* base, long long rows, long long cols, long long stride_bytes,
                      int box_rows);
+// Tensor map of a bf16 tensor of rank 2 .. 5 (dims innermost first, strides in bytes of the outer
+// dimensions), 128-byte swizzle. Encoded at each call.
+bool tensor_map_bf16_nd(CUtensorMap* map, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                        const uint32_t* box);
 // flash-style causal prefill attention on the tensor cores (attn.cu)
 bool attn_flash_supported(int D);
 cudaError_t launch_attn_flash(const uint16_t* q_hi, const uint16_t* q_lo, const uint16_t* k, const uint16_t* vt,
