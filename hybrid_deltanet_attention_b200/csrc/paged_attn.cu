@@ -7,7 +7,7 @@
 // per SM), so a single long sequence spreads over the whole GPU and ragged ones balance; a row
 // tile whose key range is cut leaves partial results (O, m, l), which a second kernel joins.
 //
-// Per key tile, with the scores in log2 units (c = scale log2 e, the sign of scale folded into q):
+// Per key tile, with the scores in log2 units (c = scale log2 e):
 //   S = Q K^T                         tcgen05, M = 128, N = 128, K = D, into TMEM
 //   m = max(m, rowmax(c S));  P = 2^(c S - m), masked above the diagonal;  l += rowsum(P)
 //   O = O + P V                       tcgen05, P (bf16) read from TMEM over the columns of S
@@ -67,7 +67,7 @@ struct AttnArgs {
   uint16_t* o;
   long long ldo;
   float c2;                // |scale| log2 e
-  uint32_t flip;           // sign of scale, for two bf16 entries
+  int negative;            // the sign of scale
   NewRows w;
   float* part;             // [2 * grid][max_rows][D]
   float2* ml;              // [2 * grid][max_rows] (m, l)
@@ -197,13 +197,13 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int i, int* bad) 
   w.seq = there ? s : 0;
   w.len = ok ? len : 0;
   w.pos0 = w.len - (e - w.row0);
-  w.row_tiles = static_cast<int>((static_cast<long long>(w.rows) * a.group + kM - 1) / kM);
+  w.row_tiles = (w.rows * a.group + kM - 1) / kM;   // below 2^30 (checked by the host)
   return w;
 }
 // Key tiles of row tile j: up to the position of its last row; one (empty) where it sees nothing.
 __device__ __forceinline__ int key_tiles(const AttnArgs& a, const SeqWork& w, int j) {
-  const long long last = min(static_cast<long long>(j + 1) * kM, static_cast<long long>(w.rows) * a.group) - 1;
-  const int keys = w.pos0 + static_cast<int>(last / a.group) + 1;
+  const int last = min((j + 1) * kM, w.rows * a.group) - 1;
+  const int keys = w.pos0 + last / a.group + 1;
   return max(1, (keys + kN - 1) / kN);
 }
 __device__ __forceinline__ SeqWork shfl_work(const SeqWork& w, int src) {
@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
         if (!whole && lane == 0) {
           int* m = a.meta + static_cast<long long>(s.part) * kMeta;
           m[0] = kPartUsed | (s.t0 == 0 ? kPartFirst : 0) | (s.t1 == tiles ? kPartLast : 0);
-          m[1] = min(kM, static_cast<int>(static_cast<long long>(w.rows) * a.group - static_cast<long long>(s.tile) * kM));
+          m[1] = min(kM, w.rows * a.group - s.tile * kM);
           m[2] = s.tile;
           m[3] = s.kvh;
           m[4] = s.row0;
@@ -489,32 +489,39 @@ __global__ void __launch_bounds__(kThreads_, 1)
     const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t it = 0, slot = 0, meets = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-      if (!warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) break;
-      const Segment s = b->seg[i % kSegs];
+    Segment s;
+    // the next segment, and its row tile's queries on their way into the swizzled layout (whose last
+    // reader, the row tile before, has computed its scores)
+    auto fetch = [&](int i) {
+      if (!warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) return false;
+      s = b->seg[i % kSegs];
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->seg_empty[i % kSegs]);
-      if (s.end) break;
-      const long long rr0 = static_cast<long long>(s.tile) * kM;
-      const int rows = static_cast<int>(min(static_cast<long long>(kM), static_cast<long long>(s.new_rows) * a.group - rr0));
-      // queries of the row tile into the swizzled layout (the previous row tile's products are done)
-      for (int v = s.len ? threadIdx.x : kM * D; v < rows * (D / 8); v += kSoftWarps * 32) {
-        const int row = v / (D / 8), e = v % (D / 8);
-        const long long rr = rr0 + row;
-        const long long tok = rr / a.group;
-        const int h = s.kvh * a.group + static_cast<int>(rr - tok * a.group);
-        uint4 x = *reinterpret_cast<const uint4*>(a.q + (s.row0 + tok) * a.ldq + static_cast<long long>(h) * D + e * 8);
-        x.x ^= a.flip, x.y ^= a.flip, x.z ^= a.flip, x.w ^= a.flip;
-        *reinterpret_cast<uint4*>(smem + (e >> 3) * kPanel + row * 128 + (((e & 7) ^ (row & 7)) << 4)) = x;
+      if (s.end || s.len == 0) return true;
+      constexpr int kLanes = D / 8, kAtOnce = kSoftWarps * 32 / kLanes;   // lanes of a row, rows at once
+      const int rows = min(kM, s.new_rows * a.group - s.tile * kM), e = threadIdx.x % kLanes;
+      for (int row = threadIdx.x / kLanes; row < rows; row += kAtOnce) {
+        const int rr = s.tile * kM + row, tok = rr / a.group, h = s.kvh * a.group + rr - tok * a.group;
+        cp_async16(smem + (e >> 3) * kPanel + row * 128 + (((e & 7) ^ (row & 7)) << 4),
+                   a.q + static_cast<long long>(s.row0 + tok) * a.ldq + h * D + e * 8, 16);
       }
+      cp_async_commit();
+      return true;
+    };
+    auto queries_in = [&] {
+      if (s.end || s.len == 0) return;
+      cp_async_wait<0>();
       tc::fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0 && s.len) mbar_arrive(&b->q_full);
+      if (lane == 0) mbar_arrive(&b->q_full);
+    };
+    bool ok = fetch(0);
+    if (ok) queries_in();
+    for (int i = 0; ok && !s.end;) {
+      const int rr0 = s.tile * kM, rows = min(kM, s.new_rows * a.group - rr0);
       const bool live = quarter * 32 < rows;       // the warp has rows of the tile
-      const long long rr = rr0 + r;
-      const int pos = s.pos0 + static_cast<int>(min(rr, rr0 + rows - 1) / a.group);
-      const int pos_first = s.pos0 + static_cast<int>((rr0 + quarter * 32) / a.group);   // the warp's lowest
+      const int tok = (rr0 + min(r, rows - 1)) / a.group, pos = s.pos0 + tok;
+      const int pos_first = s.pos0 + (rr0 + quarter * 32) / a.group;   // the warp's lowest
       float m = -INFINITY, l = 0.f;                // m in log2 units
       const int n = s.len == 0 ? 0 : s.t1 - s.t0;
       for (int j = 0; j < n; ++j, ++it) {
@@ -529,6 +536,10 @@ __global__ void __launch_bounds__(kThreads_, 1)
           tmem_ld32(sb + half * 64, x);
           tmem_ld32(sb + half * 64 + 32, x + 32);
           tmem_wait_ld();
+          if (a.negative) {
+#pragma unroll
+            for (int c = 0; c < 64; ++c) x[c] = -x[c];
+          }
           const int key0 = t * kN + half * 64;
           if (key0 + 63 > pos_first) {
 #pragma unroll
@@ -601,19 +612,23 @@ __global__ void __launch_bounds__(kThreads_, 1)
       }
       if (!ok) break;
       slot += 2u * L::kCh * n;
+      // row tile, output rows and partial slot of this segment; then the next one's queries, so that
+      // its first scores are computed during this epilogue
+      const int part = s.part;
+      const int h = s.kvh * a.group + rr0 + min(r, rows - 1) - tok * a.group;
+      uint16_t* out = a.o + static_cast<long long>(s.row0 + tok) * a.ldo + static_cast<long long>(h) * D;
+      if (!(ok = fetch(++i))) break;
       if (n > 0) {
         if (!(ok = warp_wait(b, &b->o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, err))) break;
         tc::fence_after_sync();
       }
+      queries_in();
       if (live) {
         // the halves' sums, in the buffer that the last tile did not use
         b->mx[it & 1][half][r] = l;
         if (!(ok = pair_sync(b, quarter, meets, err))) break;
         l += b->mx[it & 1][half ^ 1][r];
         if (!(ok = pair_sync(b, quarter, meets, err))) break;
-        const long long tok = rr / a.group;
-        const int h = s.kvh * a.group + static_cast<int>(rr - tok * a.group);
-        uint16_t* out = a.o + (s.row0 + tok) * a.ldo + static_cast<long long>(h) * D;
         const float inv = l > 0.f ? 1.f / l : 0.f;
         for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
           float o[32];
@@ -625,7 +640,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
             for (int k = 0; k < 32; ++k) o[k] = 0.f;
           }
           if (r < rows) {
-            if (s.part < 0) {
+            if (part < 0) {
 #pragma unroll
               for (int k = 0; k < 32; k += 8) {
                 // a row that saw nothing has l = 0 and takes exact zeros
@@ -634,16 +649,15 @@ __global__ void __launch_bounds__(kThreads_, 1)
                                pack_bf16(o[k + 4] * inv, o[k + 5] * inv), pack_bf16(o[k + 6] * inv, o[k + 7] * inv));
               }
             } else {
-              float4* dst = reinterpret_cast<float4*>(a.part + (static_cast<long long>(s.part) * a.max_rows + r) * D + c);
+              float4* dst = reinterpret_cast<float4*>(a.part + (static_cast<long long>(part) * a.max_rows + r) * D + c);
 #pragma unroll
               for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             }
           }
         }
-        if (s.part >= 0 && half == 0 && r < rows) a.ml[static_cast<long long>(s.part) * a.max_rows + r] = make_float2(m, l);
+        if (part >= 0 && half == 0 && r < rows) a.ml[static_cast<long long>(part) * a.max_rows + r] = make_float2(m, l);
         tc::fence_before_sync();
       }
-      // the queries of the next row tile overwrite these ones: every warp is past its last product
     }
   }
   tc::fence_before_sync();
@@ -721,9 +735,8 @@ __global__ void __launch_bounds__(256) join_parts(const __grid_constant__ AttnAr
         for (int e = 0; e < E; ++e) o[e] += so[warp + k][lane * E + e] * f;
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const long long rr = static_cast<long long>(tile) * kM + r, tok = rr / a.group;
-      const int h = kvh * a.group + static_cast<int>(rr - tok * a.group);
-      uint32_t* out = reinterpret_cast<uint32_t*>(a.o + (row0 + tok) * a.ldo + static_cast<long long>(h) * D + lane * E);
+      const int rr = tile * kM + r, tok = rr / a.group, h = kvh * a.group + rr - tok * a.group;
+      uint32_t* out = reinterpret_cast<uint32_t*>(a.o + static_cast<long long>(row0 + tok) * a.ldo + static_cast<long long>(h) * D + lane * E);
 #pragma unroll
       for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
     }
@@ -806,6 +819,7 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
   if (rows < 0 || n < 0 || n > 65536) return refuse("rows must not be negative, n must lie in 0 .. 65536");
   if (q_heads < 1 || q_heads % c->kv_heads) return refuse("q_heads must be a positive multiple of kv_heads");
   if (!(scale > -INFINITY && scale < INFINITY)) return refuse("scale must be finite");
+  if (static_cast<int64_t>(rows) * (q_heads / c->kv_heads) > (1 << 30)) return refuse("rows * group must be at most 2^30");
   if (rows == 0 || n == 0) return MK_OK;
   const int64_t dq = static_cast<int64_t>(q_heads) * c->head_dim;
   if (!d_q || !d_out || !d_seq_start || !d_scratch) return refuse("NULL pointer");
@@ -825,7 +839,7 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
     // masked score stays minus infinity
     const float c2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1e-30f);
     const mk::AttnArgs a{*c, layer, rows, q_heads, q_heads / c->kv_heads, box, static_cast<const uint16_t*>(d_q), ldq,
-                         static_cast<uint16_t*>(d_out), ldo, c2, std::signbit(scale) ? 0x80008000u : 0u,
+                         static_cast<uint16_t*>(d_out), ldo, c2, scale < 0 ? 1 : 0,
                          mk::NewRows{d_seq_start, d_seqs, n}, reinterpret_cast<float*>(ws), reinterpret_cast<float2*>(ws + sc.ml),
                          reinterpret_cast<int*>(ws + sc.meta), max_rows};
     CUtensorMap tk, tv;

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import math
-from typing import Optional, Tuple
+from typing import Callable, Optional, Tuple
 
 import torch
 
@@ -19,17 +19,22 @@ from ._abi import MkPagedCache, MkQkRope, check
 _DTYPES = {torch.float32: _abi.MK_DT_F32, torch.bfloat16: _abi.MK_DT_BF16}
 
 
-def _stream_of(device: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.cuda.Stream:
-    if stream is None:
-        return torch.cuda.current_stream(device)
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    return stream
-
-
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
+
+
+def _run(device: torch.device, stream: Optional[torch.cuda.Stream], body: Callable):
+    """body(raw stream) with the tensors' device current, on `stream` or the device's current stream, so that
+    what it allocates belongs to that stream. The usual case (the current device and stream) pays for no context."""
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return body(torch._C._cuda_getCurrentRawStream(device.index))
+        with torch.cuda.device(device):
+            return body(torch._C._cuda_getCurrentRawStream(device.index))
+    _need(stream.device == device, f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
 def _ints(t: torch.Tensor, what: str, device: torch.device) -> int:
@@ -38,16 +43,14 @@ def _ints(t: torch.Tensor, what: str, device: torch.device) -> int:
     return t.data_ptr()
 
 
-def _heads(t: torch.Tensor, what: str, device: torch.device, dtype, rows: int, d: int) -> None:
-    """t is [rows][heads][d], heads next to each other; rows may be strided."""
-    if (t.dim() != 3 or t.dtype != dtype or t.device != device or t.shape[0] != rows or t.shape[2] != d
-            or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+def _heads(t: torch.Tensor, what: str, device: torch.device, dtype, rows: int, d: int) -> Tuple[int, int, int]:
+    """Address, pitch and heads of t [rows][heads][d], heads next to each other; rows may be strided."""
+    shape, st = t.shape, t.stride()
+    if (len(shape) != 3 or t.dtype != dtype or t.device != device or shape[0] != rows or shape[2] != d or st[2] != 1
+            or (shape[1] > 1 and st[1] != d)):
         raise ValueError(f"{what} must be {dtype} [{rows}][heads][{d}] on {device} with its heads contiguous")
-
-
-def _pitch(t: torch.Tensor) -> int:
     # a single row has no pitch of its own; any that holds the row will do
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return t.data_ptr(), st[0] if rows > 1 else shape[1] * d, shape[1]
 
 
 def _gain(t: Optional[torch.Tensor], device: torch.device, d: int):
@@ -96,7 +99,9 @@ class PagedCache:
         c.table, c.len, c.ref = table.data_ptr(), len.data_ptr(), ref.data_ptr()
         c.work, c.err = self.work.data_ptr(), self.err.data_ptr()
         self._p = C.byref(c)
+        self._d, self._kv_heads, self._n_seqs = c.head_dim, c.kv_heads, c.n_seqs
         self._scale = 1.0 / math.sqrt(c.head_dim)
+        self._scratch = (-1, -1, 0)
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, kv_heads: int, page_size: int, head_dim: int, n_seqs: int, max_pages: int,
@@ -116,29 +121,25 @@ class PagedCache:
         self._movable()
         s, l = _ints(seqs, "seqs", self.device), _ints(lens, "lens", self.device)   # noqa: E741
         _need(seqs.numel() == lens.numel(), "seqs and lens differ in length")
-        with torch.cuda.device(self.device):
-            check(self.lib.mk_pages_resize(self._p, s, l, seqs.numel(), _stream_of(self.device, stream).cuda_stream))
+        _run(self.device, stream, lambda st: check(self.lib.mk_pages_resize(self._p, s, l, seqs.numel(), st)))
 
     def free(self, seqs: torch.Tensor, stream=None) -> None:
         """Give back every page of these sequences."""
         self._movable()
         s = _ints(seqs, "seqs", self.device)
-        with torch.cuda.device(self.device):
-            check(self.lib.mk_pages_resize(self._p, s, None, seqs.numel(), _stream_of(self.device, stream).cuda_stream))
+        _run(self.device, stream, lambda st: check(self.lib.mk_pages_resize(self._p, s, None, seqs.numel(), st)))
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Make sequence dst[i] a continuation of src[i], sharing its full pages (mk_pages_fork)."""
         self._movable()
         a, b = _ints(src, "src", self.device), _ints(dst, "dst", self.device)
         _need(src.numel() == dst.numel(), "src and dst differ in length")
-        with torch.cuda.device(self.device):
-            check(self.lib.mk_pages_fork(self._p, a, b, src.numel(), _stream_of(self.device, stream).cuda_stream))
+        _run(self.device, stream, lambda st: check(self.lib.mk_pages_fork(self._p, a, b, src.numel(), st)))
 
     def compact(self, stream=None) -> None:
         """Move the used pages to the lowest ids (mk_pages_compact)."""
         self._movable()
-        with torch.cuda.device(self.device):
-            check(self.lib.mk_pages_compact(self._p, _stream_of(self.device, stream).cuda_stream))
+        _run(self.device, stream, lambda st: check(self.lib.mk_pages_compact(self._p, st)))
 
     def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, source: Optional["PagedCache"] = None, stream=None) -> None:
         """Copy page src[i] of `source` (or of this cache) to page dst[i] of this cache (mk_pages_copy)."""
@@ -146,8 +147,7 @@ class PagedCache:
         _need(f.device == self.device, "the caches are on different devices")
         a, b = _ints(src, "src", self.device), _ints(dst, "dst", self.device)
         _need(src.numel() == dst.numel(), "src and dst differ in length")
-        with torch.cuda.device(self.device):
-            check(self.lib.mk_pages_copy(f._p, self._p, a, b, src.numel(), _stream_of(self.device, stream).cuda_stream))
+        _run(self.device, stream, lambda st: check(self.lib.mk_pages_copy(f._p, self._p, a, b, src.numel(), st)))
 
     # ---- new tokens ----
     def append(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_start: torch.Tensor,
@@ -157,35 +157,36 @@ class PagedCache:
         """Norm (where a gain is given) and rotate the queries and keys of new rows and store keys and values in
         their pages (mk_qk_norm_rope). Rows seq_start[i] .. seq_start[i+1]-1 are the last positions of sequence
         seqs[i] (or i), whose length already counts them. Returns the bfloat16 queries."""
-        c = self._c
         return _rope(self.device, q, k, v, None, q_gain, k_gain, eps, theta, rot_dim, out, None, self, layer, seq_start, seqs,
-                     c.head_dim, stream)[0]
+                     self._d, stream)[0]
 
     def attention(self, layer: int, q: torch.Tensor, seq_start: torch.Tensor, seqs: Optional[torch.Tensor] = None, *,
                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Causal attention of new rows over their sequences' pages (mk_paged_attention); q bfloat16
         [rows][query heads][head dim], scale 1/sqrt(head dim) unless given. Returns bfloat16 like q."""
-        c, dev = self._c, self.device
-        rows = q.shape[0]
-        _heads(q, "q", dev, torch.bfloat16, rows, c.head_dim)
-        start, ids, n = _new_rows(seq_start, seqs, c, dev)
-        st = _stream_of(dev, stream)
-        with torch.cuda.device(dev), torch.cuda.stream(st):
-            if out is None:
-                out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-            else:
-                _heads(out, "out", dev, torch.bfloat16, rows, c.head_dim)
-                _need(out.shape == q.shape, "out must have q's shape")
-            need = self.lib.mk_paged_attention_scratch(self._p, rows, q.shape[1])
-            scratch = torch.empty(max(16, need), dtype=torch.uint8, device=dev)
-            check(self.lib.mk_paged_attention(self._p, layer, q.data_ptr(), _pitch(q), rows, q.shape[1], start, ids, n,
-                                              self._scale if scale is None else scale, out.data_ptr(), _pitch(out),
-                                              scratch.data_ptr(), scratch.numel(), st.cuda_stream))
-        return out
+        dev, shape = self.device, q.shape
+        rows = shape[0]
+        qp, ldq, hq = _heads(q, "q", dev, torch.bfloat16, rows, self._d)
+        start, ids, n = _new_rows(seq_start, seqs, self._n_seqs, dev)
+        if out is not None:
+            op, ldo, ho = _heads(out, "out", dev, torch.bfloat16, rows, self._d)
+            _need(ho == hq, "out must have q's shape")
+
+        def body(st):
+            o, p, ld = (out, op, ldo) if out is not None else (q.new_empty(shape), 0, hq * self._d)
+            if self._scratch[:2] != (rows, hq):      # bytes for calls of this shape
+                self._scratch = (rows, hq, max(16, self.lib.mk_paged_attention_scratch(self._p, rows, hq)))
+            size = self._scratch[2]
+            scratch = torch.empty(size, dtype=torch.uint8, device=dev)
+            check(self.lib.mk_paged_attention(self._p, layer, qp, ldq, rows, hq, start, ids, n, self._scale if scale is None else scale,
+                                              p or o.data_ptr(), ld, scratch.data_ptr(), size, st))
+            return o
+
+        return _run(dev, stream, body)
 
     def sync(self, stream=None) -> None:
         """Wait for the stream and raise if a call found bad ids, lengths or too few pages (the word is then cleared)."""
-        _stream_of(self.device, stream).synchronize()
+        (stream if stream is not None else torch.cuda.current_stream(self.device)).synchronize()
         bits = int(self.err.item())
         if bits:
             self.err.zero_()
@@ -195,56 +196,52 @@ class PagedCache:
             raise _abi.MkError(_abi.MK_ERR_DEVICE, f"paged cache: {', '.join(names)} (device word 0x{bits:x})")
 
 
-def _new_rows(seq_start, seqs, c, dev) -> Tuple[int, Optional[int], int]:
+def _new_rows(seq_start, seqs, n_seqs, dev) -> Tuple[int, Optional[int], int]:
     start = _ints(seq_start, "seq_start", dev)
     n = seq_start.shape[0] - 1
     _need(n >= 0, "seq_start must have one entry more than there are sequences")
     if seqs is None:
-        _need(n <= c.n_seqs, "more sequences than the cache has")
+        _need(n <= n_seqs, "more sequences than the cache has")
         return start, None, n
     _need(seqs.shape[0] == n, "seqs must have one entry less than seq_start")
     return start, _ints(seqs, "seqs", dev), n
 
 
 def _rope(dev, q, k, v, positions, q_gain, k_gain, eps, theta, rot_dim, q_out, k_out, cache, layer, seq_start, seqs, d, stream):
-    dt = _DTYPES.get(q.dtype)
+    dtype, rows = q.dtype, q.shape[0]
+    dt = _DTYPES.get(dtype)
     _need(dt is not None, "q must be float32 or bfloat16")
-    _need(q.dim() == 3 and k.dim() == 3, "q and k must be [rows][heads][head dim]")
-    rows = q.shape[0]
-    _heads(q, "q", dev, q.dtype, rows, d)
-    _heads(k, "k", dev, q.dtype, rows, d)
-    a = MkQkRope()
-    a.dtype, a.rows, a.q_heads, a.kv_heads, a.head_dim = dt, rows, q.shape[1], k.shape[1], d
-    a.rot_dim = d if rot_dim is None else rot_dim
-    a.eps, a.theta = eps, theta
-    a.q, a.ldq, a.k, a.ldk = q.data_ptr(), _pitch(q), k.data_ptr(), _pitch(k)
-    a.q_gain, a.k_gain = _gain(q_gain, dev, d), _gain(k_gain, dev, d)
+    qp, ldq, hq = _heads(q, "q", dev, dtype, rows, d)
+    kp, ldk, hkv = _heads(k, "k", dev, dtype, rows, d)
+    vp = ldv = pos = start = ids = cp = None
+    n = 0
     if cache is not None:
-        _heads(v, "v", dev, q.dtype, rows, d)
-        _need(k.shape[1] == cache._c.kv_heads and v.shape[1] == cache._c.kv_heads, "k and v must have the cache's heads")
-        a.v, a.ldv = v.data_ptr(), _pitch(v)
-        a.seq_start, a.seqs, a.n = _new_rows(seq_start, seqs, cache._c, dev)
-        a.cache, a.layer = C.addressof(cache._c), layer
+        vp, ldv, hv = _heads(v, "v", dev, dtype, rows, d)
+        _need(hkv == cache._kv_heads and hv == hkv, "k and v must have the cache's heads")
+        start, ids, n = _new_rows(seq_start, seqs, cache._n_seqs, dev)
+        cp = C.addressof(cache._c)
     else:
-        a.positions = _ints(positions, "positions", dev)
+        pos = _ints(positions, "positions", dev)
         _need(positions.shape[0] == rows, "one position per row")
-    st = _stream_of(dev, stream)
-    with torch.cuda.device(dev), torch.cuda.stream(st):
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        else:
-            _heads(q_out, "the query output", dev, torch.bfloat16, rows, d)
-            _need(q_out.shape == q.shape, "the query output must have q's shape")
-        a.q_out, a.ldq_out = q_out.data_ptr(), _pitch(q_out)
-        if cache is None:
-            if k_out is None:
-                k_out = torch.empty(k.shape, dtype=torch.bfloat16, device=dev)
-            else:
-                _heads(k_out, "the key output", dev, torch.bfloat16, rows, d)
-                _need(k_out.shape == k.shape, "the key output must have k's shape")
-            a.k_out, a.ldk_out = k_out.data_ptr(), _pitch(k_out)
-        check(_abi.load_library().mk_qk_norm_rope(C.byref(a), st.cuda_stream))
-    return q_out, k_out
+    gq, gk = _gain(q_gain, dev, d), _gain(k_gain, dev, d)
+
+    def result(t, like, heads, what):
+        if t is None:
+            t = torch.empty(like.shape, dtype=torch.bfloat16, device=dev)
+            return t, t.data_ptr(), heads * d
+        p, ld, h = _heads(t, what, dev, torch.bfloat16, rows, d)
+        _need(h == heads, f"{what} must have its input's shape")
+        return t, p, ld
+
+    def body(st):
+        qo, qop, ldqo = result(q_out, q, hq, "the query output")
+        ko, kop, ldko = result(k_out, k, hkv, "the key output") if cache is None else (None, None, 0)
+        a = MkQkRope(dt, rows, hq, hkv, d, d if rot_dim is None else rot_dim, theta, eps, qp, ldq, kp, ldk, vp, ldv or 0, gq, gk,
+                     qop, ldqo, kop, ldko, pos, cp, layer, n, start, ids)
+        check(_abi.load_library().mk_qk_norm_rope(C.byref(a), st))
+        return qo, ko
+
+    return _run(dev, stream, body)
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, *, q_gain: Optional[torch.Tensor] = None,
