@@ -40,6 +40,7 @@ constexpr int kM = 128, kN = 128;        // rows and keys of a tile
 constexpr int kSoftWarps = 8;
 constexpr int kThreads_ = 384;
 constexpr int kSegs = 4;                 // segments the scheduler runs ahead
+constexpr int kOver = 2;                 // what a row tile costs beside its key tiles (queries in, results out), in key tiles
 constexpr float kRaise = 8.0f;           // log2 units
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kPanel = 128 * 128;        // 64 bf16 entries of 128 rows: 16 KB
@@ -93,11 +94,11 @@ struct Segment {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_done[2], q_full, pair[4], seg_full[kSegs], seg_empty[kSegs];
+  uint64_t full[8], empty[8], s_full[2], p_full[2], o_done[2], q_full, pair[4], m_full[2][4], seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem;
   int abort;
   Segment seg[kSegs];
-  float mx[2][2][kM];      // [tile parity][half][row]; also takes l at the end of a row tile
+  float m[2][kM], l[2][kM];   // [softmax group][row]
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barriers fit their slot");
 
@@ -114,7 +115,16 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Wait for the loads issued so far; v are the registers of one of them, used after the wait only.
+__device__ __forceinline__ void tmem_wait_ld(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]),
+                 "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                 "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]),
+                 "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
@@ -124,23 +134,52 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
       "r"(r[31])
       : "memory");
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// D (TMEM) += A (TMEM, bf16 pairs in 32-bit columns) * B (shared memory).
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// Values as they lie in a slot: entries of a position contiguous (MN-major), 128-byte swizzle: panels of 64
-// entries kPanel bytes apart (leading offset), groups of 8 positions 1024 bytes apart (stride).
-__device__ __forceinline__ uint64_t desc_mnmajor_sw128(const void* p) {
-  const uint32_t a = smem_u32(p);
-  return static_cast<uint64_t>((a >> 4) & 0x3FFF) | static_cast<uint64_t>(kPanel >> 4) << 16 |
-         static_cast<uint64_t>(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// The MMAs are issued by a whole warp that stays converged, the instruction itself by its elected lane, so
+// that descriptors live in uniform registers (one lane branching off costs more issue slots per
+// MMA than the MMA takes). A descriptor is a constant high word and the address in the low one.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;   // groups of 8 rows 1024 bytes apart, version, 128-byte swizzle
+constexpr uint32_t kLoK = 1u << 16;                   // K-major: leading offset unused
+constexpr uint32_t kLoMN = (kPanel >> 4) << 16;       // MN-major: panels of 64 entries kPanel bytes apart
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(issue), "r"(kDescHi)
+      : "memory");
+}
+// A from TMEM, bf16 pairs in 32-bit columns.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(issue), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t issue) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(issue)
+      : "memory");
 }
 constexpr uint32_t kBMajorMN = 1u << 16;   // instruction descriptor: B is MN-major
 
@@ -150,6 +189,37 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
           smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
+}
+// 32 bytes to a 32-byte aligned address: one store, so that a lane's row takes a whole sector.
+__device__ __forceinline__ void store32(void* p, const uint32_t* u) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]),
+               "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+// The same to a 16-byte aligned address (a row pitch may be an odd multiple of 8 entries).
+__device__ __forceinline__ void store_bf16x16(uint16_t* p, const uint32_t* u) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    store32(p, u);
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  }
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// a * b + c and a + b in both halves (packed fp32 instructions of sm_100).
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -161,11 +231,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Wait for a phase; gives up after kWaitNs or when another role did. try_wait suspends the thread in
+// hardware for a while by itself; the timer (a slow read) is looked at once in 64 attempts.
 __device__ __forceinline__ bool wait_bar(Bars* b, uint64_t* bar, uint32_t parity, int* err) {
-  if (mbar_wait(bar, parity, &b->abort, kWaitNs)) return true;
-  if (!b->abort) atomicOr(err, MK_DEVERR_PIPE_TIMEOUT);
-  b->abort = 1;
-  return false;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_test(bar, parity); ++i) {
+    if (i & 63) continue;
+    const uint64_t t = global_ns();
+    if (t0 == 0) t0 = t;
+    const bool gone = *static_cast<volatile int*>(&b->abort);
+    if (gone || t - t0 > kWaitNs) {
+      if (!gone) atomicOr(err, MK_DEVERR_PIPE_TIMEOUT);
+      *static_cast<volatile int*>(&b->abort) = 1;
+      return false;
+    }
+  }
+  return true;
 }
 __device__ __forceinline__ bool warp_wait(Bars* b, uint64_t* bar, uint32_t parity, int* err) {
   const bool ok = wait_bar(b, bar, parity, err);
@@ -215,12 +296,12 @@ __device__ long long head_units(const AttnArgs& a, const SeqWork& w) {
   const int lane = threadIdx.x & 31;
   long long u = 0;
   if (w.row_tiles <= 4)
-    for (int j = 0; j < w.row_tiles; ++j) u += key_tiles(a, w, j);
+    for (int j = 0; j < w.row_tiles; ++j) u += kOver + key_tiles(a, w, j);
   for (unsigned big = __ballot_sync(0xFFFFFFFFu, w.row_tiles > 4); big; big &= big - 1) {
     const int src = __ffs(big) - 1;
     const SeqWork x = shfl_work(w, src);
     int sum = 0;
-    for (int j = lane; j < x.row_tiles; j += 32) sum += key_tiles(a, x, j);
+    for (int j = lane; j < x.row_tiles; j += 32) sum += kOver + key_tiles(a, x, j);
     const int t = __reduce_add_sync(0xFFFFFFFFu, sum);
     if (lane == src) u = t;
   }
@@ -262,10 +343,14 @@ __global__ void __launch_bounds__(kThreads_, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b->s_full[i], 1);
-      mbar_init(&b->p_full[i], kSoftWarps);
+      mbar_init(&b->p_full[i], kSoftWarps / 2);
       mbar_init(&b->o_done[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&b->pair[i], 2);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&b->pair[i], 2);
+      mbar_init(&b->m_full[0][i], 1);
+      mbar_init(&b->m_full[1][i], 1);
+    }
     mbar_init(&b->q_full, kSoftWarps);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&b->seg_full[i], 1);
@@ -344,7 +429,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
         s.kvh = static_cast<int>(rel / h);
         int rem = static_cast<int>(rel - s.kvh * h), tiles = 0;
         for (int j0 = 0;; j0 += 32) {              // the row tile that holds unit rem of this head
-          const int t = j0 + lane < w.row_tiles ? key_tiles(a, w, j0 + lane) : 0;
+          const int t = j0 + lane < w.row_tiles ? kOver + key_tiles(a, w, j0 + lane) : 0;
           const int inc = static_cast<int>(warp_scan64(t));
           const unsigned hit = __ballot_sync(0xFFFFFFFFu, inc > rem);
           if (hit) {
@@ -356,11 +441,16 @@ __global__ void __launch_bounds__(kThreads_, 1)
           }
           rem -= __shfl_sync(0xFFFFFFFFu, inc, 31);
         }
-        s.t0 = rem;
-        s.t1 = static_cast<int>(min(static_cast<long long>(tiles), rem + (u1 - u)));
+        // tiles counts kOver units and then the key tiles; a run that ends in the former leaves the
+        // row tile to the next CTA
+        const int upto = static_cast<int>(min(static_cast<long long>(tiles), rem + (u1 - u)));
+        u += upto - rem;
+        s.t0 = max(0, rem - kOver);
+        s.t1 = upto - kOver;
+        if (s.t1 <= s.t0) continue;
+        tiles -= kOver;
         const bool whole = s.t0 == 0 && s.t1 == tiles;
         s.part = whole ? -1 : static_cast<int>(blockIdx.x) * 2 + (made ? 1 : 0);
-        u += s.t1 - s.t0;
         ++made;
         if (!whole && lane == 0) {
           int* m = a.meta + static_cast<long long>(s.part) * kMeta;
@@ -431,63 +521,72 @@ __global__ void __launch_bounds__(kThreads_, 1)
         mbar_wait(&b->full[k % L::kSlots], (k / L::kSlots) & 1, &never, kWaitNs / 10);
     }
   } else if (warp == 9) {
-    if (lane == 0) {
-      // ---- MMA issuer
-      constexpr uint32_t id_s = tc::idesc_bf16_f32(kM, kN), id_o = tc::idesc_bf16_f32(kM, L::kCW) | kBMajorMN;
-      uint32_t slot = 0, it = 0, nq = 0;
-      bool ok = true;
-      auto take = [&](uint32_t& k) {               // the next slot in order, filled
-        k = slot % L::kSlots;
-        ok = ok && wait_bar(b, &b->full[k], (slot / L::kSlots) & 1, err);
-        ++slot;
-        tc::fence_after_sync();
-        return ok;
-      };
-      auto scores = [&](uint32_t n) {             // S buffer n & 1; its P was consumed by the product before
-        const uint32_t d = tmem + L::kColS + (n & 1) * kN;
+    // ---- MMA issuer (all lanes, one issues). Values are read as they lie in a slot: MN-major.
+    constexpr uint32_t id_s = tc::idesc_bf16_f32(kM, kN), id_o = tc::idesc_bf16_f32(kM, L::kCW) | kBMajorMN;
+    const uint32_t issue = elect_lane();
+    const uint32_t q_lo = (smem_u32(smem) >> 4) | kLoK, ring_lo = smem_u32(ring) >> 4;
+    uint32_t k = 0, phase = 0, it = 0, nq = 0;     // next ring slot and its phase
+    bool ok = true;
+    auto take = [&]() {                            // wait for the next slot in order
+      ok = ok && warp_wait(b, &b->full[k], phase, err);
+      tc::fence_after_sync();
+      return ok;
+    };
+    auto pass = [&]() {                            // the slot is free once the MMAs so far are done
+      commit(&b->empty[k], issue);
+      if (++k == L::kSlots) k = 0, phase ^= 1;
+    };
+    auto scores = [&](uint32_t n) {                // S buffer n & 1; its P was consumed by the product before
+      const uint32_t d = tmem + L::kColS + (n & 1) * kN;
+#pragma unroll
+      for (int c = 0; c < L::kCh; ++c) {
+        if (!take()) return;
+        const uint32_t b_lo = (ring_lo + k * (L::kSlot >> 4)) | kLoK;
+#pragma unroll
+        for (int p = 0; p < L::kCW / 64; ++p)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ss(d, q_lo + ((c * (L::kCW / 64) + p) * kPanel + kk * 32) / 16, b_lo + (p * kPanel + kk * 32) / 16, id_s,
+                   (c | p | kk) ? 1u : 0u, issue);
+        pass();
+      }
+      commit(&b->s_full[n & 1], issue);
+    };
+    for (int i = 0; ok; ++i) {
+      if (!warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) break;
+      const int len = b->seg[i % kSegs].len, n = b->seg[i % kSegs].t1 - b->seg[i % kSegs].t0, end = b->seg[i % kSegs].end;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b->seg_empty[i % kSegs]);
+      if (end) break;
+      if (len == 0) continue;
+      if (!(ok = warp_wait(b, &b->q_full, nq++ & 1, err))) break;
+      tc::fence_after_sync();
+      scores(it);
+      for (int t = 0; t < n && ok; ++t, ++it) {
+        if (t + 1 < n) scores(it + 1);
+        if (!ok || !(ok = warp_wait(b, &b->p_full[it & 1], (it >> 1) & 1, err))) break;
+        const uint32_t pa = tmem + L::kColS + (it & 1) * kN, more = t > 0;
+#pragma unroll
         for (int c = 0; c < L::kCh; ++c) {
-          uint32_t k;
-          if (!take(k)) return;
-          for (int p = 0; p < L::kCW / 64; ++p)
+          if (!take()) break;
+          const uint32_t b_lo = (ring_lo + k * (L::kSlot >> 4)) | kLoMN;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc::mma_bf16(d, tc::desc_kmajor_sw128(smem + (c * (L::kCW / 64) + p) * kPanel + kk * 32),
-                           tc::desc_kmajor_sw128(ring + k * L::kSlot + p * kPanel + kk * 32), id_s, (c | p | kk) ? 1u : 0u);
-          tc::mma_commit(&b->empty[k]);
+          for (int kk = 0; kk < kN / 16; ++kk)
+            mma_ts(tmem + c * L::kCW, pa + kk * 8, b_lo + kk * (2048 / 16), id_o, kk ? 1u : more, issue);
+          pass();
         }
-        tc::mma_commit(&b->s_full[n & 1]);
-      };
-      for (int i = 0; ok; ++i) {
-        if (!wait_bar(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) break;
-        const Segment s = b->seg[i % kSegs];
-        mbar_arrive(&b->seg_empty[i % kSegs]);
-        if (s.end) break;
-        if (s.len == 0) continue;
-        if (!(ok = wait_bar(b, &b->q_full, nq++ & 1, err))) break;
-        tc::fence_after_sync();
-        scores(it);
-        for (int t = s.t0; t < s.t1 && ok; ++t, ++it) {
-          if (t + 1 < s.t1) scores(it + 1);
-          if (!ok || !(ok = wait_bar(b, &b->p_full[it & 1], (it >> 1) & 1, err))) break;
-          const uint32_t pa = tmem + L::kColS + (it & 1) * kN;
-          for (int c = 0; c < L::kCh; ++c) {
-            uint32_t k;
-            if (!take(k)) break;
-#pragma unroll
-            for (int kk = 0; kk < kN / 16; ++kk)
-              mma_bf16_ts(tmem + c * L::kCW, pa + kk * 8, desc_mnmajor_sw128(ring + k * L::kSlot + kk * 2048), id_o,
-                          (t > s.t0 || kk) ? 1u : 0u);
-            tc::mma_commit(&b->empty[k]);
-          }
-          if (ok) tc::mma_commit(&b->o_done[it & 1]);
-        }
+        if (ok) commit(&b->o_done[it & 1], issue);
       }
     }
     __syncwarp();
   } else if (warp < kSoftWarps) {
-    // ---- softmax and epilogue: row r of the tile, keys half * 64 .. + 63 of each key tile
-    const int quarter = warp & 3, half = warp >> 2, r = quarter * 32 + lane;
+    // ---- softmax and epilogue: thread = row r of the tile; the warps of group 0 take the even key
+    // tiles of the CTA, those of group 1 the odd ones, so one group exponentiates while the other
+    // loads the next scores and finds their maximum. m passes from tile to tile through shared
+    // memory (published before the exponentials); each group keeps its own l.
+    const int quarter = warp & 3, grp = warp >> 2, r = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t sb = tmem + lanes + L::kColS + grp * kN;
     uint32_t it = 0, slot = 0, meets = 0;
     Segment s;
     // the next segment, and its row tile's queries on their way into the swizzled layout (whose last
@@ -522,73 +621,102 @@ __global__ void __launch_bounds__(kThreads_, 1)
       const bool live = quarter * 32 < rows;       // the warp has rows of the tile
       const int tok = (rr0 + min(r, rows - 1)) / a.group, pos = s.pos0 + tok;
       const int pos_first = s.pos0 + (rr0 + quarter * 32) / a.group;   // the warp's lowest
-      float m = -INFINITY, l = 0.f;                // m in log2 units
       const int n = s.len == 0 ? 0 : s.t1 - s.t0;
+      float l = 0.f, ml = -INFINITY;               // this group's sum, and the m (log2 units) it goes by
       for (int j = 0; j < n; ++j, ++it) {
-        const int t = s.t0 + j, buf = it & 1;
-        if (!(ok = warp_wait(b, &b->s_full[buf], (it >> 1) & 1, err))) break;
-        // long done (it was issued before these scores), but a parity wait must not skip a phase
-        if (it >= 2 && !(ok = warp_wait(b, &b->o_done[buf], ((it >> 1) - 1) & 1, err))) break;
+        if ((it & 1) != static_cast<uint32_t>(grp)) continue;
+        const int t = s.t0 + j;
+        if (!(ok = warp_wait(b, &b->s_full[grp], (it >> 1) & 1, err))) break;
+        // long done (issued before these scores), but a parity wait must not skip a phase
+        if (it >= 2 && !(ok = warp_wait(b, &b->o_done[grp], ((it >> 1) - 1) & 1, err))) break;
         if (live) {
           tc::fence_after_sync();
-          const uint32_t sb = tmem + lanes + L::kColS + buf * kN;
-          float x[64];
-          tmem_ld32(sb + half * 64, x);
-          tmem_ld32(sb + half * 64 + 32, x + 32);
-          tmem_wait_ld();
-          if (a.negative) {
+          const int key0 = t * kN;
+          const bool masked = key0 + kN - 1 > pos_first;
+          // scores as they enter the maximum and the exponentials: nothing to do but for masked tiles and
+          // a negative scale, so those have a branch of their own
+          const bool plain = !masked && !a.negative;
+          auto prepare = [&](int c, float* x) {
+            if (a.negative) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = -x[c];
-          }
-          const int key0 = t * kN + half * 64;
-          if (key0 + 63 > pos_first) {
+              for (int k = 0; k < 32; ++k) x[k] = -x[k];
+            }
 #pragma unroll
-            for (int c = 0; c < 64; ++c) x[c] = key0 + c <= pos ? x[c] : -INFINITY;
-          }
-          float m0 = x[0], m1 = x[1], m2 = x[2], m3 = x[3];
+            for (int k = 0; k < 32; ++k) x[k] = key0 + c + k <= pos ? x[k] : -INFINITY;
+          };
+          // the tile's 128 columns in four loads, each issued while the one before is worked on
+          auto columns = [&](auto&& work) {
+            float x[2][32];
+            tmem_ld32(sb, x[0]);
 #pragma unroll
-          for (int c = 4; c < 64; c += 4) {
-            m0 = fmaxf(m0, x[c]), m1 = fmaxf(m1, x[c + 1]);
-            m2 = fmaxf(m2, x[c + 2]), m3 = fmaxf(m3, x[c + 3]);
+            for (int c = 0; c < 4; ++c) {
+              tmem_wait_ld(x[c & 1]);
+              if (c < 3) tmem_ld32(sb + (c + 1) * 32, x[(c + 1) & 1]);
+              if (!plain) prepare(c * 32, x[c & 1]);
+              work(c, x[c & 1]);
+            }
+          };
+          float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
+          columns([&](int, const float* x) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              m0 = max3(m0, x[k], x[k + 1]), m1 = max3(m1, x[k + 2], x[k + 3]);
+              m2 = max3(m2, x[k + 4], x[k + 5]), m3 = max3(m3, x[k + 6], x[k + 7]);
+            }
+          });
+          const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * a.c2;   // -inf where the row sees none
+          float m = top;
+          bool raise = false;
+          if (j > 0) {
+            if (!(ok = warp_wait(b, &b->m_full[grp ^ 1][quarter], ((it - 1) >> 1) & 1, err))) break;
+            m = b->m[grp ^ 1][r];
+            raise = r < rows && top > m + kRaise;
           }
-          m0 = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
-          b->mx[buf][half][r] = m0;
-          tc::fence_before_sync();
-          if (!(ok = pair_sync(b, quarter, meets, err))) break;   // both halves of the scores are in registers
-          tc::fence_after_sync();
-          const float top = fmaxf(m0, b->mx[buf][half ^ 1][r]) * a.c2;   // -inf where the row sees none
-          const bool raise = r < rows && top > m + kRaise;
-          if (j == 0) {
-            m = top;
-          } else if (__any_sync(0xFFFFFFFFu, raise)) {
-            // O and l of the rows that raise are rescaled (factor 1 for the others); O is up to
-            // date once the product before has completed
-            if (!(ok = warp_wait(b, &b->o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, err))) break;
+          const float f = raise ? ex2(m - top) : 1.f;
+          if (raise) m = top;
+          b->m[grp][r] = m;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b->m_full[grp][quarter]);
+          if (__any_sync(0xFFFFFFFFu, raise)) {
+            // the warp's rows of O are rescaled (factor 1 where the row keeps its m) once the
+            // product before has completed
+            if (!(ok = warp_wait(b, &b->o_done[grp ^ 1], ((it - 1) >> 1) & 1, err))) break;
             tc::fence_after_sync();
-            const float f = raise ? ex2(m - top) : 1.f;
-            l *= f;
-            if (raise) m = top;
-            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
               float o[32];
               tmem_ld32(tmem + lanes + c, o);
-              tmem_wait_ld();
+              tmem_wait_ld(o);
               uint32_t u[32];
 #pragma unroll
               for (int k = 0; k < 32; ++k) u[k] = __float_as_uint(o[k] * f);
               tmem_st32(tmem + lanes + c, u);
             }
+            tmem_wait_st();
           }
+          if (ml != m) l *= ex2(ml - m);           // m may have been raised at the other group's tile
+          ml = m;
           const float sub = m == -INFINITY ? 0.f : -m;
-          uint32_t p[32];
-          float l0 = 0.f, l1 = 0.f;
+          const uint64_t mul = f2_pack(a.c2, a.c2), add = f2_pack(sub, sub);
+          uint64_t sum0 = 0, sum1 = 0;
+          columns([&](int c, const float* x) {
+            uint32_t p[16];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const float p0 = ex2(fmaf(x[2 * c], a.c2, sub)), p1 = ex2(fmaf(x[2 * c + 1], a.c2, sub));
-            l0 += p0, l1 += p1;
-            p[c] = pack_bf16(p0, p1);
-          }
-          l += l0 + l1;
-          tmem_st32(sb + half * 32, p);
+            for (int k = 0; k < 16; k += 2) {
+              const float2 u = f2_unpack(fma2(f2_pack(x[2 * k], x[2 * k + 1]), mul, add));
+              const float2 w = f2_unpack(fma2(f2_pack(x[2 * k + 2], x[2 * k + 3]), mul, add));
+              const float p0 = ex2(u.x), p1 = ex2(u.y), p2 = ex2(w.x), p3 = ex2(w.y);
+              sum0 = add2(sum0, f2_pack(p0, p1));
+              sum1 = add2(sum1, f2_pack(p2, p3));
+              p[k] = pack_bf16(p0, p1);
+              p[k + 1] = pack_bf16(p2, p3);
+            }
+            tmem_st16(sb + c * 16, p);             // over columns of S that have been loaded
+          });
+          tmem_wait_st();
+          l += f2_sum(add2(sum0, sum1));
+        } else if (lane == 0) {
+          mbar_arrive(&b->m_full[grp][quarter]);   // nothing to pass on, but the phases count tiles
         }
         if ((t + 1) * kN > s.len) {
           // positions from len on: whatever lies there must not meet a weight of zero as NaN
@@ -598,7 +726,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
             ok = warp_wait(b, &b->full[k], ((at + c) / L::kSlots) & 1, err);
             if (!ok) break;
             const int first = s.len - t * kN;
-            for (int v = threadIdx.x; v < (kN - first) * (L::kCW / 8); v += kSoftWarps * 32) {
+            for (int v = threadIdx.x & 127; v < (kN - first) * (L::kCW / 8); v += 128) {
               const int row = first + v / (L::kCW / 8), e = v % (L::kCW / 8);
               *reinterpret_cast<uint4*>(ring + k * L::kSlot + (e >> 3) * kPanel + row * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
@@ -608,54 +736,58 @@ __global__ void __launch_bounds__(kThreads_, 1)
         }
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->p_full[buf]);   // two barriers: a warp may be a tile ahead of another
+        if (lane == 0) mbar_arrive(&b->p_full[grp]);
       }
       if (!ok) break;
       slot += 2u * L::kCh * n;
-      // row tile, output rows and partial slot of this segment; then the next one's queries, so that
-      // its first scores are computed during this epilogue
+      // output row and partial slot of this segment; then the next one's queries, so that its first
+      // scores are computed during this epilogue
       const int part = s.part;
       const int h = s.kvh * a.group + rr0 + min(r, rows - 1) - tok * a.group;
       uint16_t* out = a.o + static_cast<long long>(s.row0 + tok) * a.ldo + static_cast<long long>(h) * D;
+      if (n > 0 && !(ok = warp_wait(b, &b->s_full[(it - 1) & 1], ((it - 1) >> 1) & 1, err))) break;
       if (!(ok = fetch(++i))) break;
+      float m = -INFINITY;
       if (n > 0) {
+        // the last product and the one before it, in order: no phase is skipped
+        if (n > 1 && !(ok = warp_wait(b, &b->o_done[it & 1], ((it - 2) >> 1) & 1, err))) break;
         if (!(ok = warp_wait(b, &b->o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, err))) break;
         tc::fence_after_sync();
       }
       queries_in();
       if (live) {
-        // the halves' sums, in the buffer that the last tile did not use
-        b->mx[it & 1][half][r] = l;
+        if (n > 0) m = b->m[(it - 1) & 1][r];      // the last tile's
+        if (ml != m) l *= ex2(ml - m);             // a group without a tile has l = 0 and ml = -inf
+        b->l[grp][r] = l;
         if (!(ok = pair_sync(b, quarter, meets, err))) break;
-        l += b->mx[it & 1][half ^ 1][r];
+        l += b->l[grp ^ 1][r];
         if (!(ok = pair_sync(b, quarter, meets, err))) break;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;   // a row that saw nothing takes exact zeros
+#pragma unroll 1
+        for (int c = grp * (D / 2); c < (grp + 1) * (D / 2); c += 32) {
           float o[32];
           if (n > 0) {
             tmem_ld32(tmem + lanes + c, o);
-            tmem_wait_ld();
+            tmem_wait_ld(o);
           } else {
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0.f;
           }
           if (r < rows) {
             if (part < 0) {
+              uint32_t u[16];
 #pragma unroll
-              for (int k = 0; k < 32; k += 8) {
-                // a row that saw nothing has l = 0 and takes exact zeros
-                *reinterpret_cast<uint4*>(out + c + k) =
-                    make_uint4(pack_bf16(o[k] * inv, o[k + 1] * inv), pack_bf16(o[k + 2] * inv, o[k + 3] * inv),
-                               pack_bf16(o[k + 4] * inv, o[k + 5] * inv), pack_bf16(o[k + 6] * inv, o[k + 7] * inv));
-              }
+              for (int k = 0; k < 16; ++k) u[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+              store_bf16x16(out + c, u);
+              store_bf16x16(out + c + 16, u + 8);
             } else {
-              float4* dst = reinterpret_cast<float4*>(a.part + (static_cast<long long>(part) * a.max_rows + r) * D + c);
+              float* dst = a.part + (static_cast<long long>(part) * a.max_rows + r) * D + c;
 #pragma unroll
-              for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              for (int k = 0; k < 32; k += 8) store32(dst + k, reinterpret_cast<const uint32_t*>(o) + k);
             }
           }
         }
-        if (part >= 0 && half == 0 && r < rows) a.ml[static_cast<long long>(part) * a.max_rows + r] = make_float2(m, l);
+        if (part >= 0 && grp == 0 && r < rows) a.ml[static_cast<long long>(part) * a.max_rows + r] = make_float2(m, l);
         tc::fence_before_sync();
       }
     }
@@ -824,7 +956,8 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
   const int64_t dq = static_cast<int64_t>(q_heads) * c->head_dim;
   if (!d_q || !d_out || !d_seq_start || !d_scratch) return refuse("NULL pointer");
   if (ldq < dq || ldo < dq || ldq % 8 || ldo % 8) return refuse("row pitches must be multiples of 8 that hold the heads");
-  if (!mk::aligned16(d_q) || !mk::aligned16(d_out) || !mk::aligned16(d_scratch)) return refuse("pointers must be 16-byte aligned");
+  if (!mk::aligned16(d_q) || !mk::aligned16(d_out) || (reinterpret_cast<uintptr_t>(d_scratch) & 31))
+    return refuse("d_q and d_out must be 16-byte, d_scratch 32-byte aligned");
   const int max_rows = mk::max_rows_of(c, rows, q_heads);
   const size_t least = mk::scratch_of(1, max_rows, c->head_dim).total;
   if (scratch_bytes < least) return refuse("scratch too small");
