@@ -16,7 +16,7 @@
 // are fp32; a weight is rounded to bf16 once, as an operand, and the result once, at the end.
 //
 // Roles of the 12 warps: 0-7 softmax (two warps per 32 rows, each half of the tile's keys) and
-// epilogue, 8 TMA producer, 9 MMA issuer, 10 scheduler. Keys and values go through a ring of
+// epilogue, 8 and 11 TMA producers (keys, values), 9 MMA issuer, 10 scheduler. Keys and values go through a ring of
 // shared-memory slots (128 keys x min(D, 128) entries), filled by TMA boxes that follow the page table (a
 // box is the largest power of two of slots that divides the page size, at most 128); the order
 // K0 K1 V0 K2 V1 ... is the order of use, and it runs on across row tiles, so memory stays busy through
@@ -183,7 +183,8 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t issue) {
 }
 constexpr uint32_t kBMajorMN = 1u << 16;   // instruction descriptor: B is MN-major
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+// One box of a 4-D tensor map.
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
           smem_u32(dst)),
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
     mbar_init(&b->q_full, kSoftWarps);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&b->seg_full[i], 1);
-      mbar_init(&b->seg_empty[i], kSoftWarps + 2);
+      mbar_init(&b->seg_empty[i], kSoftWarps + 3);
     }
     fence_barrier_init();
   }
@@ -392,9 +393,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
     for (; g + 1 < n_groups && before + groups[g] <= u0; ++g) before += groups[g];
   }
   tc::fence_proxy_async_smem();
-  __syncthreads();   // the ring is the producer's from here
+  __syncthreads();   // the ring is the producers' from here
   const uint32_t tmem = b->tmem;
-
+  // registers: 256 x 208 + 128 x 88 = 384 x 168, what the CTA was launched with
+  if (warp >= kSoftWarps) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == 10) {
     // ---- scheduler: cut [u0, u1) into segments
     int emitted = 0, made = 0;
@@ -467,59 +470,64 @@ __global__ void __launch_bounds__(kThreads_, 1)
     Segment stop{};
     stop.end = 1;
     if (ok) emit(stop);
-  } else if (warp == 8) {
-    // ---- TMA producer
-    uint32_t slot = 0;   // slots filled so far
-    bool ok = true;
+  } else if (warp == 8 || warp == 11) {
+    // ---- TMA producers, of the keys and of the values. Lane i loads box i of a tile: its page is read
+    // two tiles ahead and checked one tile ahead of the load that uses it.
+    const bool is_v = warp == 11;
+    const CUtensorMap* map = is_v ? &tv : &tk;
     const int per_tile = kN / a.box;
-    auto load = [&](const Segment& s, const CUtensorMap* map, int tile, int page) {
-      // lane i < per_tile holds the page of box i of the tile (-1: past the sequence's end)
-      const int valid = min(per_tile, (s.len - tile * kN + a.box - 1) / a.box);
-      for (int c = 0; c < L::kCh; ++c, ++slot) {
-        const uint32_t k = slot % L::kSlots;
-        if (slot >= L::kSlots) ok = ok && warp_wait(b, &b->empty[k], (slot / L::kSlots - 1) & 1, err);
-        if (!ok) return;
-        if (lane == 0) mbar_arrive_expect_tx(&b->full[k], valid * a.box * L::kCW * 2);
-        __syncwarp();
-        if (lane < valid) {
-          const int at = (tile * kN + lane * a.box) % a.c.page_size;
-          for (int p = 0; p < L::kCW / 64; ++p)
-            tma_load_4d(ring + k * L::kSlot + p * kPanel + lane * a.box * 128, map, c * L::kCW + p * 64, at, s.kvh, page, &b->full[k]);
-        }
-      }
-    };
+    uint32_t base = 0, last = 0;                   // ring slots before the segment; the last one filled, plus one
+    bool ok = true;
     for (int i = 0; ok; ++i) {
       if (!warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) break;
       const Segment s = b->seg[i % kSegs];
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->seg_empty[i % kSegs]);
       if (s.end) break;
-      const int* row = a.c.table + static_cast<long long>(s.seq) * a.c.max_pages;
-      auto page_of = [&](int tile) {
-        const int p = tile * kN + lane * a.box;
-        if (tile >= s.t1 || lane >= per_tile || p >= s.len) return -1;
-        const int page = row[p / a.c.page_size];
-        if (page >= 0 && page < a.c.n_pages) return page;
-        atomicOr(err, MK_DEVERR_BAD_PAGE);
-        return a.c.n_pages;                        // outside the tensor map: reads as zeros
-      };
       if (s.len == 0) continue;                    // nothing to read
-      // page ids one tile ahead of the loads that use them
-      int now = page_of(s.t0), next = page_of(s.t0 + 1);
-      load(s, &tk, s.t0, now);
-      for (int t = s.t0; t < s.t1 && ok; ++t) {
-        const int after = page_of(t + 2);
-        if (t + 1 < s.t1) load(s, &tk, t + 1, next);
-        if (ok) load(s, &tv, t, now);
+      const int* row = a.c.table + static_cast<long long>(s.seq) * a.c.max_pages;
+      const int n = s.t1 - s.t0;
+      auto raw_page = [&](int tile) {
+        const int p = tile * kN + lane * a.box;
+        return tile < s.t1 && lane < per_tile && p < s.len ? row[p / a.c.page_size] : 0;
+      };
+      int now = raw_page(s.t0), next = raw_page(s.t0 + 1);
+      for (int j = 0; j < n && ok; ++j) {
+        const int t = s.t0 + j;
+        const int after = raw_page(t + 2);
+        if (now < 0 || now >= a.c.n_pages) {
+          atomicOr(err, MK_DEVERR_BAD_PAGE);
+          now = a.c.n_pages;                       // outside the tensor map: reads as zeros
+        }
+        const int boxes = min(per_tile, (s.len - t * kN + a.box - 1) / a.box);   // up to the sequence's end
+        const int y = (t * kN + lane * a.box) % a.c.page_size;                   // a box never crosses a page
+        // place of the tile in the order K0 K1 V0 K2 V1 ... (the ring's releases come in this order too, and a
+        // producer is never more than kSlots past its last wait, so no phase is skipped)
+        const uint32_t at = base + L::kCh * (is_v ? (j < n - 1 ? 2 * j + 2 : 2 * n - 1) : j ? 2 * j - 1 : 0);
+        for (int c = 0; c < L::kCh && ok; ++c) {
+          const uint32_t slot = at + c, k = slot % L::kSlots;
+          if (slot >= L::kSlots) ok = warp_wait(b, &b->empty[k], (slot / L::kSlots - 1) & 1, err);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&b->full[k], boxes * a.box * L::kCW * 2);
+          __syncwarp();
+          if (lane < boxes) {
+#pragma unroll
+            for (int p = 0; p < L::kCW / 64; ++p)
+              tma_box(ring + k * L::kSlot + p * kPanel + lane * a.box * 128, map, c * L::kCW + p * 64, y, s.kvh, now, &b->full[k]);
+          }
+          last = slot + 1;
+        }
         now = next;
         next = after;
       }
+      base += 2u * L::kCh * n;
     }
     if (!ok && lane == 0) {                        // copies in flight land before the CTA ends (bounded)
       int never = 0;
-      for (uint32_t k = slot < L::kSlots ? 0u : slot - L::kSlots; k < slot; ++k)
-        mbar_wait(&b->full[k % L::kSlots], (k / L::kSlots) & 1, &never, kWaitNs / 10);
+      for (uint32_t i = last < L::kSlots ? 0u : last - L::kSlots; i < last; ++i)
+        mbar_wait(&b->full[i % L::kSlots], (i / L::kSlots) & 1, &never, kWaitNs / 10);
     }
+    __syncwarp();
   } else if (warp == 9) {
     // ---- MMA issuer (all lanes, one issues). Values are read as they lie in a slot: MN-major.
     constexpr uint32_t id_s = tc::idesc_bf16_f32(kM, kN), id_o = tc::idesc_bf16_f32(kM, L::kCW) | kBMajorMN;
@@ -579,7 +587,9 @@ __global__ void __launch_bounds__(kThreads_, 1)
       }
     }
     __syncwarp();
-  } else if (warp < kSoftWarps) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ---- softmax and epilogue: thread = row r of the tile; the warps of group 0 take the even key
     // tiles of the CTA, those of group 1 the odd ones, so one group exponentiates while the other
     // loads the next scores and finds their maximum. m passes from tile to tile through shared
@@ -633,37 +643,26 @@ __global__ void __launch_bounds__(kThreads_, 1)
           tc::fence_after_sync();
           const int key0 = t * kN;
           const bool masked = key0 + kN - 1 > pos_first;
-          // scores as they enter the maximum and the exponentials: nothing to do but for masked tiles and
-          // a negative scale, so those have a branch of their own
-          const bool plain = !masked && !a.negative;
-          auto prepare = [&](int c, float* x) {
-            if (a.negative) {
+          // the row's 128 scores stay in registers: four loads in flight, and one pass for the maximum
+          float x[kN];
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = -x[k];
-            }
+          for (int c = 0; c < kN; c += 32) tmem_ld32(sb + c, x + c);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = key0 + c + k <= pos ? x[k] : -INFINITY;
-          };
-          // the tile's 128 columns in four loads, each issued while the one before is worked on
-          auto columns = [&](auto&& work) {
-            float x[2][32];
-            tmem_ld32(sb, x[0]);
+          for (int c = 0; c < kN; c += 32) tmem_wait_ld(x + c);
+          if (a.negative) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_wait_ld(x[c & 1]);
-              if (c < 3) tmem_ld32(sb + (c + 1) * 32, x[(c + 1) & 1]);
-              if (!plain) prepare(c * 32, x[c & 1]);
-              work(c, x[c & 1]);
-            }
-          };
+            for (int c = 0; c < kN; ++c) x[c] = -x[c];
+          }
+          if (masked) {
+#pragma unroll
+            for (int c = 0; c < kN; ++c) x[c] = key0 + c <= pos ? x[c] : -INFINITY;
+          }
           float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
-          columns([&](int, const float* x) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              m0 = max3(m0, x[k], x[k + 1]), m1 = max3(m1, x[k + 2], x[k + 3]);
-              m2 = max3(m2, x[k + 4], x[k + 5]), m3 = max3(m3, x[k + 6], x[k + 7]);
-            }
-          });
+          for (int c = 0; c < kN; c += 8) {
+            m0 = max3(m0, x[c], x[c + 1]), m1 = max3(m1, x[c + 2], x[c + 3]);
+            m2 = max3(m2, x[c + 4], x[c + 5]), m3 = max3(m3, x[c + 6], x[c + 7]);
+          }
           const float top = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * a.c2;   // -inf where the row sees none
           float m = top;
           bool raise = false;
@@ -699,20 +698,21 @@ __global__ void __launch_bounds__(kThreads_, 1)
           const float sub = m == -INFINITY ? 0.f : -m;
           const uint64_t mul = f2_pack(a.c2, a.c2), add = f2_pack(sub, sub);
           uint64_t sum0 = 0, sum1 = 0;
-          columns([&](int c, const float* x) {
+#pragma unroll
+          for (int c = 0; c < kN; c += 32) {
             uint32_t p[16];
 #pragma unroll
             for (int k = 0; k < 16; k += 2) {
-              const float2 u = f2_unpack(fma2(f2_pack(x[2 * k], x[2 * k + 1]), mul, add));
-              const float2 w = f2_unpack(fma2(f2_pack(x[2 * k + 2], x[2 * k + 3]), mul, add));
+              const float2 u = f2_unpack(fma2(f2_pack(x[c + 2 * k], x[c + 2 * k + 1]), mul, add));
+              const float2 w = f2_unpack(fma2(f2_pack(x[c + 2 * k + 2], x[c + 2 * k + 3]), mul, add));
               const float p0 = ex2(u.x), p1 = ex2(u.y), p2 = ex2(w.x), p3 = ex2(w.y);
               sum0 = add2(sum0, f2_pack(p0, p1));
               sum1 = add2(sum1, f2_pack(p2, p3));
               p[k] = pack_bf16(p0, p1);
               p[k + 1] = pack_bf16(p2, p3);
             }
-            tmem_st16(sb + c * 16, p);             // over columns of S that have been loaded
-          });
+            tmem_st16(sb + c / 2, p);              // over the scores, which have all been loaded
+          }
           tmem_wait_st();
           l += f2_sum(add2(sum0, sum1));
         } else if (lane == 0) {
