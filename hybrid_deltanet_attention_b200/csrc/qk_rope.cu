@@ -2,12 +2,16 @@
 // the pages of a cache, in one pass: every projection entry is read once and every result
 // written once, so many rows are bound by HBM and one row by the latency of its dependent loads.
 //
-// One CTA per row, one warp per head: a lane holds head_dim / 32 consecutive entries, so loads
-// and stores are one 8- to 32-byte vector a lane and the mean of squares is one warp sum. The
+// A warp takes up to eight heads of one row, fewer (down to one) when there are too few rows to fill
+// the GPU, and has the next head on its way while it works on one. A lane holds head_dim / 32 consecutive entries, so
+// loads and stores are one 8- to 32-byte vector a lane and the mean of squares is one warp sum. The
 // rotation partner of entry i is entry i + rot_dim / 2, which lies 16 rot_dim / head_dim lanes on
-// at the same place in the lane: one shuffle per entry. The row's angles are shared by
-// all heads: position * theta^(-2i / rot_dim) in float64, reduced to [-pi, pi] there, sine and
-// cosine in fp32, kept in shared memory.
+// at the same place in the lane: one shuffle per entry. The angles of the row, position *
+// theta^(-2i / rot_dim) in float64, reduced to half a turn there, sine and cosine in fp32, are
+// computed once per warp while the first heads are on their way; two lanes that are partners share
+// their angles, so each computes half of them (one float64 power, the others by the common ratio: at
+// most three more roundings of 2^-53).
+#include <algorithm>
 #include <cmath>
 #include <string>
 
@@ -19,11 +23,12 @@
 namespace mk {
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 struct RopeArgs {
   int rows, hq, hkv, rot;
-  double log2_theta;
+  int parts;               // warps that share a row's heads
+  double log2_ratio, ratio;   // theta^(-2 / rot_dim)
   float eps;
   const void *q, *k, *v;
   long long ldq, ldk, ldv;
@@ -84,17 +89,33 @@ __device__ __forceinline__ void store_row(uint16_t* p, const float* x) {
     *reinterpret_cast<uint32_t*>(p) = u[0];
 }
 
+constexpr double kLog2TwoPi = 2.6514961294723187980432933;
+
+// Cosine and sine of pos * per turns: the whole turns are dropped in float64 (positions are large), so
+// the fp32 functions see at most half a turn.
+__device__ __forceinline__ void turn_cs(int pos, double per, float& c, float& s) {
+  const double t = pos * per;
+  sincospif(static_cast<float>(2.0 * (t - rint(t))), &s, &c);
+}
+
+constexpr int kHeads = 8;   // heads of a warp, at most
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int E = D / 32;
-  __shared__ float2 cs[D / 2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  const long long task = blockIdx.x * static_cast<long long>(kRopeThreads / 32) + (threadIdx.x >> 5);
+  const int r = static_cast<int>(task / a.parts), part = static_cast<int>(task - static_cast<long long>(r) * a.parts);
+  if (r >= a.rows) return;
   const bool paged = a.positions == nullptr;
+  const int heads = a.hq + a.hkv * (paged ? 2 : 1);
+  const int h0 = static_cast<int>(static_cast<long long>(heads) * part / a.parts);
+  const int h1 = static_cast<int>(static_cast<long long>(heads) * (part + 1) / a.parts);
   int pos;
   uint16_t *krow = nullptr, *vrow = nullptr;   // this row's slot of head 0
   bool ok = true;
   if (paged) {
-    if (r < a.w.start[0] || r >= a.w.start[a.w.n]) return;   // the same for the whole CTA
+    if (r < a.w.start[0] || r >= a.w.start[a.w.n]) return;   // the same for the whole warp
     const int i = find_rows(a.w, r), s = a.w.seqs ? a.w.seqs[i] : i;
     ok = s >= 0 && s < a.c.n_seqs;
     pos = ok ? a.c.len[s] - a.w.start[i + 1] + r : 0;
@@ -105,73 +126,86 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
       const long long at = a.layer * a.c.layer_stride + page * a.c.page_stride + (pos % a.c.page_size) * a.c.slot_stride;
       krow = static_cast<uint16_t*>(a.c.k) + at;
       vrow = static_cast<uint16_t*>(a.c.v) + at;
-    } else if (threadIdx.x == 0) {
+    } else if (lane == 0) {
       atomicOr(a.c.err, MK_DEVERR_BAD_PAGE);
     }
   } else {
     pos = a.positions[r];
   }
-  const int half = a.rot / 2;
-  for (int i = threadIdx.x; i < half; i += kRopeThreads) {
-    const double freq = exp2(-2.0 * i / a.rot * a.log2_theta);
-    float c, s;
-    rope_cs(pos * freq, c, s);
-    cs[i] = make_float2(c, s);
-  }
-  __syncthreads();
-  const int shift = half / E;                        // lanes between rotation partners
+  const int half = a.rot / 2, shift = half / E;      // entries and lanes between rotation partners
   const bool first = lane < shift, turn = lane < 2 * shift;
   const int partner = first ? lane + shift : turn ? lane - shift : lane;
   float co[E], si[E];                                // this lane's angles; the first half subtracts
+  // the first lane of a pair computes its first E/2 angles, the second one the others
+  double per = turn ? exp2(((first ? lane : lane - shift) * E + (first ? 0 : E / 2)) * a.log2_ratio - kLog2TwoPi) : 0.0;
 #pragma unroll
-  for (int j = 0; j < E; ++j) {
-    const float2 t = turn ? cs[(first ? lane : lane - shift) * E + j] : make_float2(1.f, 0.f);
-    co[j] = t.x;
-    si[j] = first ? -t.y : t.y;
+  for (int j = 0; j < E / 2; ++j) {
+    float c, s;
+    turn_cs(pos, per, c, s);                         // lanes that do not turn: cosine 1, sine 0
+    per *= a.ratio;
+    const float oc = __shfl_sync(0xFFFFFFFFu, c, partner), os = __shfl_sync(0xFFFFFFFFu, s, partner);
+    co[j] = first ? c : oc;
+    co[j + E / 2] = first ? oc : c;
+    si[j] = first ? -s : os;
+    si[j + E / 2] = first ? -os : s;
   }
-  const int heads = a.hq + a.hkv * (paged ? 2 : 1);
-  for (int h = warp; h < heads; h += kRopeThreads / 32) {
-    const bool is_q = h < a.hq, is_v = h >= a.hq + a.hkv;
-    const int hh = is_q ? h : is_v ? h - a.hq - a.hkv : h - a.hq;
-    const T* src = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) + r * (is_q ? a.ldq : is_v ? a.ldv : a.ldk) + hh * D;
-    uint16_t* dst = is_q ? a.qo + r * a.ldqo + hh * D
-                    : !paged ? a.ko + r * a.ldko + hh * D
-                    : !ok ? nullptr
-                          : (is_v ? vrow : krow) + hh * a.c.head_stride;
-    if (!dst) continue;
-    float x[E];
-    load_row<E>(src + lane * E, x);
-    if (!is_v) {
-      const uint16_t* gain = is_q ? a.gq : a.gk;
+  // heads [i0, i1) of one kind (queries, keys, values), the next one on its way
+  const bool whole = a.rot == D;
+  auto work = [&](const void* from, long long ld, uint16_t* to, long long step, const uint16_t* gain, bool rotate, int i0, int i1) {
+    if (i0 >= i1) return;
+    const T* src = static_cast<const T*>(from) + r * ld + lane * E;
+    float x[E], next[E], g[E];
+    load_row<E>(src + i0 * D, next);
+    if (gain) load_row<E>(gain + lane * E, g);
+    to += lane * E;
+    for (int i = i0; i < i1; ++i) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) x[j] = next[j];
+      if (i + 1 < i1) load_row<E>(src + (i + 1) * D, next);
       if (gain) {
-        float g[E], ss = 0.f;
-        load_row<E>(gain + lane * E, g);
+        float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < E; ++j) ss = fmaf(x[j], x[j], ss);
         const float inv = rsqrtf(warp_sum(ss) * (1.0f / D) + a.eps);
 #pragma unroll
         for (int j = 0; j < E; ++j) x[j] *= inv * g[j];
       }
+      if (rotate) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        const float y = __shfl_sync(0xFFFFFFFFu, x[j], partner);
-        if (turn) x[j] = fmaf(x[j], co[j], y * si[j]);
+        for (int j = 0; j < E; ++j) {
+          const float y = __shfl_sync(0xFFFFFFFFu, x[j], partner), z = fmaf(x[j], co[j], y * si[j]);
+          x[j] = whole || turn ? z : x[j];
+        }
       }
-    }
-    if (!ok) {
+      if (!ok) {
 #pragma unroll
-      for (int j = 0; j < E; ++j) x[j] = 0.f;
+        for (int j = 0; j < E; ++j) x[j] = 0.f;
+      }
+      store_row<E>(to + i * step, x);
     }
-    store_row<E>(dst + lane * E, x);
+  };
+  const int hk = a.hq + a.hkv;
+  work(a.q, a.ldq, a.qo + r * a.ldqo, D, a.gq, true, h0, min(h1, a.hq));
+  if (!paged) {
+    work(a.k, a.ldk, a.ko + r * a.ldko, D, a.gk, true, max(h0 - a.hq, 0), h1 - a.hq);
+  } else if (ok) {
+    work(a.k, a.ldk, krow, a.c.head_stride, a.gk, true, max(h0 - a.hq, 0), min(h1 - a.hq, a.hkv));
+    work(a.v, a.ldv, vrow, a.c.head_stride, nullptr, false, max(h0 - hk, 0), h1 - hk);
   }
 }
 
 template <int D>
-cudaError_t launch_rope(const RopeArgs& a, bool f32, cudaStream_t s) {
+cudaError_t launch_rope(RopeArgs a, bool f32, cudaStream_t s) {
+  const int heads = a.hq + a.hkv * (a.positions ? 1 : 2);
+  int per = kHeads;   // heads of a warp, halved until the GPU has 16 warps per SM
+  while (per > 1 && static_cast<long long>(a.rows) * ((heads + per - 1) / per) < 148 * 16) per /= 2;
+  a.parts = (heads + per - 1) / per;
+  const long long warps = static_cast<long long>(a.rows) * a.parts;
+  const int grid = static_cast<int>((warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
   if (f32)
-    qk_norm_rope_kernel<D, float><<<a.rows, kRopeThreads, 0, s>>>(a);
+    qk_norm_rope_kernel<D, float><<<grid, kRopeThreads, 0, s>>>(a);
   else
-    qk_norm_rope_kernel<D, uint16_t><<<a.rows, kRopeThreads, 0, s>>>(a);
+    qk_norm_rope_kernel<D, uint16_t><<<grid, kRopeThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -212,7 +246,7 @@ extern "C" int mk_qk_norm_rope(const mk_qk_rope* a, void* stream) {
     return refuse("pointers must be 16-byte aligned");
   mk::RopeArgs r{};
   r.rows = a->rows, r.hq = a->q_heads, r.hkv = a->kv_heads, r.rot = a->rot_dim;
-  r.log2_theta = std::log2(a->theta), r.eps = a->eps;
+  r.log2_ratio = a->rot_dim ? -2.0 / a->rot_dim * std::log2(a->theta) : 0.0, r.ratio = std::exp2(r.log2_ratio), r.eps = a->eps;
   r.q = a->q, r.k = a->k, r.v = a->v, r.ldq = a->ldq, r.ldk = a->ldk, r.ldv = a->ldv;
   r.gq = static_cast<const uint16_t*>(a->q_gain), r.gk = static_cast<const uint16_t*>(a->k_gain);
   r.qo = static_cast<uint16_t*>(a->q_out), r.ldqo = a->ldq_out;

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import math
+import struct
 from typing import Callable, Optional, Tuple
 
 import torch
@@ -17,6 +18,11 @@ from . import _abi
 from ._abi import MkPagedCache, MkQkRope, check
 
 _DTYPES = {torch.float32: _abi.MK_DT_F32, torch.bfloat16: _abi.MK_DT_BF16}
+_BF16 = torch.bfloat16
+_raw_stream = torch._C._cuda_getCurrentRawStream
+# mk_qk_rope in one piece (filling a ctypes structure field by field costs more than the call)
+_ROPE = struct.Struct("@6idf4xPqPqPqPPPqPqPPiiPP")
+assert _ROPE.size == C.sizeof(MkQkRope)
 
 
 def _need(ok: bool, what: str) -> None:
@@ -29,35 +35,34 @@ def _run(device: torch.device, stream: Optional[torch.cuda.Stream], body: Callab
     what it allocates belongs to that stream. The usual case (the current device and stream) pays for no context."""
     if stream is None:
         if torch.cuda.current_device() == device.index:
-            return body(torch._C._cuda_getCurrentRawStream(device.index))
+            return body(_raw_stream(device.index))
         with torch.cuda.device(device):
-            return body(torch._C._cuda_getCurrentRawStream(device.index))
+            return body(_raw_stream(device.index))
     _need(stream.device == device, f"the stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.stream(stream):
         return body(stream.cuda_stream)
 
 
-def _ints(t: torch.Tensor, what: str, device: torch.device) -> int:
-    if t.dtype != torch.int32 or t.dim() != 1 or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous 1-D int32 tensor on {device}")
+# Tensors are compared by device index here: every caller has made sure that the index means CUDA.
+def _ints(t: torch.Tensor, what: str, index: int) -> int:
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous 1-D int32 tensor on cuda:{index}")
     return t.data_ptr()
 
 
-def _heads(t: torch.Tensor, what: str, device: torch.device, dtype, rows: int, d: int) -> Tuple[int, int, int]:
+def _heads(t: torch.Tensor, what: str, index: int, dtype, rows: int, d: int) -> Tuple[int, int, int]:
     """Address, pitch and heads of t [rows][heads][d], heads next to each other; rows may be strided."""
     shape, st = t.shape, t.stride()
-    if (len(shape) != 3 or t.dtype != dtype or t.device != device or shape[0] != rows or shape[2] != d or st[2] != 1
+    if (len(shape) != 3 or t.dtype is not dtype or t.get_device() != index or shape[0] != rows or shape[2] != d or st[2] != 1
             or (shape[1] > 1 and st[1] != d)):
-        raise ValueError(f"{what} must be {dtype} [{rows}][heads][{d}] on {device} with its heads contiguous")
+        raise ValueError(f"{what} must be {dtype} [{rows}][heads][{d}] on cuda:{index} with its heads contiguous")
     # a single row has no pitch of its own; any that holds the row will do
     return t.data_ptr(), st[0] if rows > 1 else shape[1] * d, shape[1]
 
 
-def _gain(t: Optional[torch.Tensor], device: torch.device, d: int):
-    if t is None:
-        return None
-    if t.dtype != torch.bfloat16 or t.shape != (d,) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"a gain must be a contiguous bfloat16 tensor of {d} on {device}")
+def _gain(t: torch.Tensor, index: int, d: int) -> int:
+    if t.dtype is not _BF16 or t.shape != (d,) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"a gain must be a contiguous bfloat16 tensor of {d} on cuda:{index}")
     return t.data_ptr()
 
 
@@ -83,7 +88,7 @@ class PagedCache:
         _need(len.shape[0] == table.shape[0], "table and len disagree in the number of sequences")
         _need(ref.shape[0] == k.shape[1], "ref must have one entry per page")
         self.k, self.v, self.table, self.len, self.ref = k, v, table, len, ref
-        self.device = k.device
+        self.device, self._index = k.device, k.get_device()
         c = self._c = MkPagedCache()
         c.k, c.v = k.data_ptr(), v.data_ptr()
         c.n_layers, c.n_pages, c.kv_heads, c.page_size, c.head_dim = k.shape
@@ -98,10 +103,11 @@ class PagedCache:
         self.work = torch.zeros(int(self.lib.mk_pages_work_ints(C.byref(c))), dtype=torch.int32, device=k.device)
         c.table, c.len, c.ref = table.data_ptr(), len.data_ptr(), ref.data_ptr()
         c.work, c.err = self.work.data_ptr(), self.err.data_ptr()
-        self._p = C.byref(c)
+        self._p, self._address = C.byref(c), C.addressof(c)
         self._d, self._kv_heads, self._n_seqs = c.head_dim, c.kv_heads, c.n_seqs
         self._scale = 1.0 / math.sqrt(c.head_dim)
         self._scratch = (-1, -1, 0)
+        self._bytes = torch.empty(0, dtype=torch.uint8, device=k.device)
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, kv_heads: int, page_size: int, head_dim: int, n_seqs: int, max_pages: int,
@@ -119,20 +125,20 @@ class PagedCache:
     def resize(self, seqs: torch.Tensor, lens: torch.Tensor, stream=None) -> None:
         """Set the lengths of different sequences, taking and giving back pages (mk_pages_resize)."""
         self._movable()
-        s, l = _ints(seqs, "seqs", self.device), _ints(lens, "lens", self.device)   # noqa: E741
+        s, l = _ints(seqs, "seqs", self._index), _ints(lens, "lens", self._index)   # noqa: E741
         _need(seqs.numel() == lens.numel(), "seqs and lens differ in length")
         _run(self.device, stream, lambda st: check(self.lib.mk_pages_resize(self._p, s, l, seqs.numel(), st)))
 
     def free(self, seqs: torch.Tensor, stream=None) -> None:
         """Give back every page of these sequences."""
         self._movable()
-        s = _ints(seqs, "seqs", self.device)
+        s = _ints(seqs, "seqs", self._index)
         _run(self.device, stream, lambda st: check(self.lib.mk_pages_resize(self._p, s, None, seqs.numel(), st)))
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Make sequence dst[i] a continuation of src[i], sharing its full pages (mk_pages_fork)."""
         self._movable()
-        a, b = _ints(src, "src", self.device), _ints(dst, "dst", self.device)
+        a, b = _ints(src, "src", self._index), _ints(dst, "dst", self._index)
         _need(src.numel() == dst.numel(), "src and dst differ in length")
         _run(self.device, stream, lambda st: check(self.lib.mk_pages_fork(self._p, a, b, src.numel(), st)))
 
@@ -145,7 +151,7 @@ class PagedCache:
         """Copy page src[i] of `source` (or of this cache) to page dst[i] of this cache (mk_pages_copy)."""
         f = self if source is None else source
         _need(f.device == self.device, "the caches are on different devices")
-        a, b = _ints(src, "src", self.device), _ints(dst, "dst", self.device)
+        a, b = _ints(src, "src", self._index), _ints(dst, "dst", self._index)
         _need(src.numel() == dst.numel(), "src and dst differ in length")
         _run(self.device, stream, lambda st: check(self.lib.mk_pages_copy(f._p, self._p, a, b, src.numel(), st)))
 
@@ -164,25 +170,24 @@ class PagedCache:
                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Causal attention of new rows over their sequences' pages (mk_paged_attention); q bfloat16
         [rows][query heads][head dim], scale 1/sqrt(head dim) unless given. Returns bfloat16 like q."""
-        dev, shape = self.device, q.shape
-        rows = shape[0]
-        qp, ldq, hq = _heads(q, "q", dev, torch.bfloat16, rows, self._d)
-        start, ids, n = _new_rows(seq_start, seqs, self._n_seqs, dev)
+        index, rows = self._index, q.shape[0]
+        qp, ldq, hq = _heads(q, "q", index, _BF16, rows, self._d)
+        start, ids, n = _new_rows(seq_start, seqs, self._n_seqs, index)
         if out is not None:
-            op, ldo, ho = _heads(out, "out", dev, torch.bfloat16, rows, self._d)
+            op, ldo, ho = _heads(out, "out", index, _BF16, rows, self._d)
             _need(ho == hq, "out must have q's shape")
 
         def body(st):
-            o, p, ld = (out, op, ldo) if out is not None else (q.new_empty(shape), 0, hq * self._d)
+            o, p, ld = (out, op, ldo) if out is not None else (torch.empty_like(q), 0, hq * self._d)
             if self._scratch[:2] != (rows, hq):      # bytes for calls of this shape
-                self._scratch = (rows, hq, max(16, self.lib.mk_paged_attention_scratch(self._p, rows, hq)))
+                self._scratch = (rows, hq, max(32, self.lib.mk_paged_attention_scratch(self._p, rows, hq)))
             size = self._scratch[2]
-            scratch = torch.empty(size, dtype=torch.uint8, device=dev)
+            scratch = self._bytes.new_empty(size)
             check(self.lib.mk_paged_attention(self._p, layer, qp, ldq, rows, hq, start, ids, n, self._scale if scale is None else scale,
                                               p or o.data_ptr(), ld, scratch.data_ptr(), size, st))
             return o
 
-        return _run(dev, stream, body)
+        return _run(self.device, stream, body)
 
     def sync(self, stream=None) -> None:
         """Wait for the stream and raise if a call found bad ids, lengths or too few pages (the word is then cleared)."""
@@ -196,49 +201,51 @@ class PagedCache:
             raise _abi.MkError(_abi.MK_ERR_DEVICE, f"paged cache: {', '.join(names)} (device word 0x{bits:x})")
 
 
-def _new_rows(seq_start, seqs, n_seqs, dev) -> Tuple[int, Optional[int], int]:
-    start = _ints(seq_start, "seq_start", dev)
+def _new_rows(seq_start, seqs, n_seqs, index) -> Tuple[int, Optional[int], int]:
+    start = _ints(seq_start, "seq_start", index)
     n = seq_start.shape[0] - 1
     _need(n >= 0, "seq_start must have one entry more than there are sequences")
     if seqs is None:
         _need(n <= n_seqs, "more sequences than the cache has")
         return start, None, n
     _need(seqs.shape[0] == n, "seqs must have one entry less than seq_start")
-    return start, _ints(seqs, "seqs", dev), n
+    return start, _ints(seqs, "seqs", index), n
 
 
 def _rope(dev, q, k, v, positions, q_gain, k_gain, eps, theta, rot_dim, q_out, k_out, cache, layer, seq_start, seqs, d, stream):
-    dtype, rows = q.dtype, q.shape[0]
+    dtype, rows, index = q.dtype, q.shape[0], dev.index
     dt = _DTYPES.get(dtype)
     _need(dt is not None, "q must be float32 or bfloat16")
-    qp, ldq, hq = _heads(q, "q", dev, dtype, rows, d)
-    kp, ldk, hkv = _heads(k, "k", dev, dtype, rows, d)
-    vp = ldv = pos = start = ids = cp = None
-    n = 0
+    qp, ldq, hq = _heads(q, "q", index, dtype, rows, d)
+    kp, ldk, hkv = _heads(k, "k", index, dtype, rows, d)
+    vp = ldv = pos = start = ids = cp = n = qop = kop = ldko = 0
     if cache is not None:
-        vp, ldv, hv = _heads(v, "v", dev, dtype, rows, d)
+        vp, ldv, hv = _heads(v, "v", index, dtype, rows, d)
         _need(hkv == cache._kv_heads and hv == hkv, "k and v must have the cache's heads")
-        start, ids, n = _new_rows(seq_start, seqs, cache._n_seqs, dev)
-        cp = C.addressof(cache._c)
+        start, ids, n = _new_rows(seq_start, seqs, cache._n_seqs, index)
+        cp = cache._address
     else:
-        pos = _ints(positions, "positions", dev)
+        pos = _ints(positions, "positions", index)
         _need(positions.shape[0] == rows, "one position per row")
-    gq, gk = _gain(q_gain, dev, d), _gain(k_gain, dev, d)
-
-    def result(t, like, heads, what):
-        if t is None:
-            t = torch.empty(like.shape, dtype=torch.bfloat16, device=dev)
-            return t, t.data_ptr(), heads * d
-        p, ld, h = _heads(t, what, dev, torch.bfloat16, rows, d)
-        _need(h == heads, f"{what} must have its input's shape")
-        return t, p, ld
+        ldko = hkv * d
+        if k_out is not None:
+            kop, ldko, h = _heads(k_out, "the key output", index, _BF16, rows, d)
+            _need(h == hkv, "the key output must have k's shape")
+    ldqo = hq * d
+    if q_out is not None:
+        qop, ldqo, h = _heads(q_out, "the query output", index, _BF16, rows, d)
+        _need(h == hq, "the query output must have q's shape")
+    gq = 0 if q_gain is None else _gain(q_gain, index, d)
+    gk = 0 if k_gain is None else _gain(k_gain, index, d)
 
     def body(st):
-        qo, qop, ldqo = result(q_out, q, hq, "the query output")
-        ko, kop, ldko = result(k_out, k, hkv, "the key output") if cache is None else (None, None, 0)
-        a = MkQkRope(dt, rows, hq, hkv, d, d if rot_dim is None else rot_dim, theta, eps, qp, ldq, kp, ldk, vp, ldv or 0, gq, gk,
-                     qop, ldqo, kop, ldko, pos, cp, layer, n, start, ids)
-        check(_abi.load_library().mk_qk_norm_rope(C.byref(a), st))
+        # a fresh output is contiguous: the heads of a row are, and rows that are further apart are packed
+        qo = q_out if q_out is not None else torch.empty_like(q, dtype=_BF16)
+        ko = k_out if k_out is not None or cache is not None else torch.empty_like(k, dtype=_BF16)
+        a = _ROPE.pack(dt, rows, hq, hkv, d, d if rot_dim is None else rot_dim, theta, eps, qp, ldq, kp, ldk, vp, ldv, gq, gk,
+                       qop or qo.data_ptr(), ldqo, 0 if cache is not None else kop or ko.data_ptr(), ldko, pos, cp, layer, n, start,
+                       ids or 0)
+        check(_abi.load_library().mk_qk_norm_rope(a, st))
         return qo, ko
 
     return _run(dev, stream, body)
