@@ -64,26 +64,87 @@ __device__ T block_scan(T v, T* total, T* red) {
   return base + x - v;
 }
 
-// Ranks the free pages below n_pages in ascending order into list until `want` are found;
-// returns how many there are (at most about want + one chunk are looked at).
-__device__ int list_free(const mk_paged_cache& c, int want, int* list, int* red) {
-  constexpr int kPer = 8;
+// The use counts and the list of free pages while a plan works on them: copies in shared memory for up
+// to kRefCached / kListCached pages (scattered counts, and entries that are read right after they were
+// written, each cost an L2 round trip otherwise), the arrays themselves beyond that.
+constexpr int kRefCached = 48 * 1024, kListCached = 24 * 1024;
+struct Counts {
+  int* p;
+  int n;
+  bool cached;
+  __device__ int at(long long i) const { return cached ? p[i] : __ldcg(p + i); }
+};
+// Asynchronous: cp_async_wait and a barrier before the first use.
+__device__ Counts open_counts(const mk_paged_cache& c, int* cache) {
+  if (c.n_pages > kRefCached) return Counts{c.ref, c.n_pages, false};
+  const bool wide = (reinterpret_cast<uintptr_t>(c.ref) & 15) == 0;
+  const int quads = wide ? c.n_pages / 4 : 0;
+  for (int i = threadIdx.x; i < quads; i += kPlanThreads) cp_async16(cache + 4 * i, c.ref + 4 * i, 16);
+  for (int i = 4 * quads + threadIdx.x; i < c.n_pages; i += kPlanThreads) cp_async4(cache + i, c.ref + i, 4);
+  cp_async_commit();
+  return Counts{cache, c.n_pages, true};
+}
+// After the block's last change (and a barrier).
+__device__ void close_counts(const mk_paged_cache& c, const Counts& r) {
+  if (!r.cached) return;
+  const bool wide = (reinterpret_cast<uintptr_t>(c.ref) & 15) == 0;
+  const int quads = wide ? c.n_pages / 4 : 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < quads; i += kPlanThreads) reinterpret_cast<int4*>(c.ref)[i] = reinterpret_cast<const int4*>(r.p)[i];
+  for (int i = 4 * quads + threadIdx.x; i < c.n_pages; i += kPlanThreads) c.ref[i] = r.p[i];
+}
+
+// Ranks the free pages in ascending order into list until `want` are found; returns how many
+// there are (at most about want + one chunk are looked at). A lane looks at four consecutive counts at a
+// time, two such steps to a chunk of 8192 pages.
+template <bool kCachedCounts>
+__device__ int list_free(const Counts& ref, int want, int* list, int* red) {
+  constexpr int kSteps = 2;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned below = (1u << lane) - 1u;
+  const bool wide = kCachedCounts || (reinterpret_cast<uintptr_t>(ref.p) & 15) == 0;
   int found = 0;
-  for (long long base = 0; base < c.n_pages && found < want; base += kPlanThreads * kPer) {
-    const long long p0 = base + threadIdx.x * kPer;
-    unsigned free = 0;
+  for (long long base = 0; base < ref.n && found < want; base += kPlanThreads * 4 * kSteps) {
+    const int p0 = static_cast<int>(base) + warp * 128 * kSteps + lane * 4;   // below 2^31: n_pages is an int
+    unsigned mine[kSteps], before[kSteps], all[kSteps];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (p0 + j < c.n_pages && c.ref[p0 + j] == 0) free |= 1u << j;
-    int total;
-    int r = found + block_scan(__popc(free), &total, red);
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      if (free >> j & 1) {
-        if (r < want) list[r] = static_cast<int>(p0 + j);
-        ++r;
+    for (int k = 0; k < kSteps; ++k) {
+      const int p = p0 + 128 * k;
+      int4 v = make_int4(1, 1, 1, 1);
+      if (wide && p <= ref.n - 4) {
+        v = kCachedCounts ? *reinterpret_cast<const int4*>(ref.p + p) : __ldcg(reinterpret_cast<const int4*>(ref.p + p));
+      } else if (p >= 0) {
+        if (p < ref.n) v.x = ref.at(p);
+        if (p < ref.n - 1) v.y = ref.at(p + 1);
+        if (p < ref.n - 2) v.z = ref.at(p + 2);
+        if (p < ref.n - 3) v.w = ref.at(p + 3);
       }
-    found += total;
+      mine[k] = (v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3;
+      before[k] = all[k] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const unsigned b = __ballot_sync(0xFFFFFFFFu, mine[k] >> j & 1);
+        before[k] += __popc(b & below);
+        all[k] += __popc(b);
+      }
+    }
+    __syncthreads();   // the totals of the chunk before have been read
+    if (lane == 0) red[warp] = all[0] + all[1];
+    __syncthreads();
+    const int t = red[lane];   // kPlanWarps == 32
+    int r = found + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? t : 0);
+    found += __reduce_add_sync(0xFFFFFFFFu, t);
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      int at = r + before[k];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (mine[k] >> j & 1) {
+          if (at < want) list[at] = p0 + 128 * k + j;
+          ++at;
+        }
+      r += all[k];
+    }
   }
   __syncthreads();
   return found;
@@ -91,12 +152,13 @@ __device__ int list_free(const mk_paged_cache& c, int want, int* list, int* red)
 
 // Scan of need[0 .. n) in place (exclusive); returns the sum, which may be far above what an
 // offset can be (offsets are only used when the sum is at most n_pages).
-__device__ long long scan_need(int* need, int n, long long* red) {
+template <typename T>
+__device__ long long scan_need(int* need, int n, T* red) {
   long long sum = 0;
   for (int base = 0; base < n; base += kPlanThreads) {
     const int i = base + threadIdx.x;
-    long long total;
-    const long long off = sum + block_scan<long long>(i < n ? need[i] : 0, &total, red);
+    T total;
+    const long long off = sum + block_scan<T>(i < n ? need[i] : 0, &total, red);
     if (i < n) need[i] = static_cast<int>(min(off, 0x7fffffffll));
     sum += total;
   }
@@ -106,167 +168,244 @@ __device__ long long scan_need(int* need, int n, long long* red) {
 
 __device__ __forceinline__ bool len_ok(const mk_paged_cache& c, int n) { return n >= 0 && n <= c.max_pages * c.page_size; }
 
-// mk_pages_resize. Phases, a block barrier between them: check everything; give back the
+// What a plan keeps of each of its sequences: in shared memory for up to kCached of them,
+// beyond that it reads the arrays again (and keeps need and own in the scratch).
+constexpr int kCached = 1024;
+struct Plan {
+  int a[kCached], from[kCached], to[kCached], from_pages[kCached], to_pages[kCached], need[kCached], own[kCached];
+  int red[32];
+  long long red64[32];
+};
+
+// f(j, p) for the entries p of table columns first .. last - 1 of a row, by one warp; four loads in flight.
+template <typename F>
+__device__ __forceinline__ void for_row(const int* row, int first, int last, F&& f) {
+  for (int j0 = first + (threadIdx.x & 31); j0 < last; j0 += 128) {
+    int p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) p[k] = j0 + 32 * k < last ? row[j0 + 32 * k] : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (j0 + 32 * k < last) f(j0 + 32 * k, p[k]);
+  }
+}
+
+// Adds `by` to the counts of the pages in columns first .. last - 1; true where an entry names no page.
+__device__ __forceinline__ bool count_row(const mk_paged_cache& c, const Counts& ref, int s, int first, int last, int by) {
+  bool bad = false;
+  for_row(c.table + static_cast<long long>(s) * c.max_pages, first, last, [&](int, int p) {
+    if (p >= 0 && p < c.n_pages)
+      atomicAdd(&ref.p[p], by);
+    else
+      bad = true;
+  });
+  return bad;
+}
+
+// Each sequence at most once: the last writer's index stands in mark, every other one finds it.
+__device__ __forceinline__ bool named_twice(const Work& w, int s, int i) { return __ldcg(&w.mark[s]) != i; }
+
+// mk_pages_resize. Phases, a block barrier between them: check ids and lengths; give back the
 // pages past each new end; count what each sequence takes (a shared partly filled page that stays
 // is replaced: its count is read after every release and before any replacement); rank the
-// free pages, or undo; write table, counts and lengths.
-__global__ void __launch_bounds__(kPlanThreads) plan_resize(mk_paged_cache c, const int* seqs, const int* lens, int n) {
-  __shared__ int red[32];
-  __shared__ long long red64[32];
+// free pages; write table, counts and lengths. A bad entry or too few pages take the releases back.
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_resize(mk_paged_cache c, const int* seqs, const int* lens, int n) {
+  __shared__ Plan sm;
+  extern __shared__ __align__(16) int counts[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copy kernel comes up meanwhile
   const Work w = work_of(c);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ps = c.page_size;
+  const bool small = n <= kCached;
+  int* need = small ? sm.need : w.need;
+  int* own = small ? sm.own : w.mark;
+  auto get = [&](int i, int& s, int& op, int& np) {   // pages before and after
+    if (small) {
+      s = sm.a[i], op = sm.from_pages[i], np = sm.to_pages[i];
+    } else {
+      s = seqs[i], op = pages_of(c.len[s], ps), np = pages_of(lens ? lens[i] : 0, ps);
+    }
+  };
+  const Counts ref = open_counts(c, counts);
+  int* list = c.n_pages <= kListCached ? counts + ((c.n_pages + 3) & ~3) : w.list;
   if (tid == 0) w.count[0] = 0;
-  for (int i = tid; i < c.n_seqs; i += kPlanThreads) w.mark[i] = 0;
-  __syncthreads();
   int bad = 0;
   for (int i = tid; i < n; i += kPlanThreads) {
-    const int s = seqs[i];
-    if (s < 0 || s >= c.n_seqs || atomicAdd(&w.mark[s], 1) || !len_ok(c, c.len[s]) || (lens && !len_ok(c, lens[i]))) bad = 1;
+    const int s = seqs[i], now = lens ? lens[i] : 0;
+    const bool there = s >= 0 && s < c.n_seqs;
+    const int old = there ? c.len[s] : 0;
+    bad |= !there || !len_ok(c, old) || !len_ok(c, now);
+    if (there) w.mark[s] = i;
+    if (small) sm.a[i] = s, sm.from[i] = old, sm.to[i] = now, sm.from_pages[i] = pages_of(old, ps), sm.to_pages[i] = pages_of(now, ps);
   }
-  if (__syncthreads_or(bad)) {
+  cp_async_wait<0>();
+  if (!__syncthreads_or(bad)) {
+    for (int i = tid; i < n; i += kPlanThreads) bad |= named_twice(w, small ? sm.a[i] : seqs[i], i);
+    bad = __syncthreads_or(bad);
+  } else {
+    bad = 1;
+  }
+  if (bad) {
     if (tid == 0) atomicOr(c.err, MK_DEVERR_BAD_PAGE);
     return;
   }
-  // a sequence is one warp's: columns [first, last) are the entries the call touches
+  // a sequence is one warp's
   for (int i = warp; i < n; i += kPlanWarps) {
-    const int s = seqs[i], old = c.len[s], now = lens ? lens[i] : 0;
-    const int* row = c.table + static_cast<long long>(s) * c.max_pages;
-    for (int j = min(old, now) / ps + lane; j < pages_of(old, ps); j += 32)
-      if (row[j] < 0 || row[j] >= c.n_pages) bad = 1;
-  }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) atomicOr(c.err, MK_DEVERR_BAD_PAGE);
-    return;
-  }
-  for (int i = warp; i < n; i += kPlanWarps) {
-    const int s = seqs[i], old = c.len[s], now = lens ? lens[i] : 0;
-    const int* row = c.table + static_cast<long long>(s) * c.max_pages;
-    for (int j = pages_of(now, ps) + lane; j < pages_of(old, ps); j += 32) atomicSub(&c.ref[row[j]], 1);
+    int s, op, np;
+    get(i, s, op, np);
+    bad |= count_row(c, ref, s, np, op, -1);
   }
   __syncthreads();
   for (int i = tid; i < n; i += kPlanThreads) {
-    const int s = seqs[i], now = lens ? lens[i] : 0, low = min(c.len[s], now);
-    int need = max(0, pages_of(now, ps) - pages_of(low, ps));
-    const bool own = low % ps && c.ref[c.table[static_cast<long long>(s) * c.max_pages + low / ps]] > 1;
-    w.mark[s] = own;
-    w.need[i] = need + own;
-  }
-  __syncthreads();
-  const long long total = scan_need(w.need, n, red64);
-  const int want = static_cast<int>(min(total, static_cast<long long>(c.n_pages) + 1));
-  if (list_free(c, want, w.list, red) < total) {   // nothing changes: take the releases back
-    for (int i = warp; i < n; i += kPlanWarps) {
-      const int s = seqs[i], old = c.len[s], now = lens ? lens[i] : 0;
-      const int* row = c.table + static_cast<long long>(s) * c.max_pages;
-      for (int j = pages_of(now, ps) + lane; j < pages_of(old, ps); j += 32) atomicAdd(&c.ref[row[j]], 1);
+    const int s = small ? sm.a[i] : seqs[i];
+    const int old = small ? sm.from[i] : c.len[s], now = small ? sm.to[i] : lens ? lens[i] : 0;
+    const int low = min(old, now);
+    int mine = 0;
+    if (low % ps) {
+      const int p = c.table[static_cast<long long>(s) * c.max_pages + low / ps];
+      if (p < 0 || p >= c.n_pages)
+        bad = 1;
+      else
+        mine = ref.at(p) > 1;
     }
-    if (tid == 0) atomicOr(c.err, MK_DEVERR_NO_PAGES);
+    own[i] = mine;
+    need[i] = max(0, pages_of(now, ps) - pages_of(low, ps)) + mine;
+  }
+  bad = __syncthreads_or(bad);
+  // 1024 of these fit 32 bits in any table of less than 2^21 columns
+  const long long total = bad ? 0 : c.max_pages < (1 << 20) ? scan_need(need, n, sm.red) : scan_need(need, n, sm.red64);
+  const int want = static_cast<int>(min(total, static_cast<long long>(c.n_pages) + 1));
+  if (bad || (ref.cached ? list_free<true>(ref, want, list, sm.red) : list_free<false>(ref, want, list, sm.red)) < total) {   // nothing changes: take the releases back
+    for (int i = warp; i < n; i += kPlanWarps) {
+      int s, op, np;
+      get(i, s, op, np);
+      count_row(c, ref, s, np, op, 1);
+    }
+    if (tid == 0) atomicOr(c.err, bad ? MK_DEVERR_BAD_PAGE : MK_DEVERR_NO_PAGES);
     return;
   }
   for (int i = warp; i < n; i += kPlanWarps) {
-    const int s = seqs[i], old = c.len[s], now = lens ? lens[i] : 0, low = min(old, now);
+    int s, op, np;
+    get(i, s, op, np);
+    const int mine = own[i], have = min(op, np);
     int* row = c.table + static_cast<long long>(s) * c.max_pages;
-    const int own = w.mark[s], have = pages_of(low, ps), np = pages_of(now, ps);
-    const int* take = w.list + w.need[i];
-    if (own && lane == 0) {
-      const int e = low / ps, was = row[e], now_p = take[0], at = atomicAdd(&w.count[0], 1);
+    const int* take = list + need[i];
+    if (mine && lane == 0) {
+      const int low = min(c.len[s], lens ? lens[i] : 0);
+      const int e = low / ps, was = row[e], page = take[0], at = atomicAdd(&w.count[0], 1);
       w.src[at] = was;
-      w.dst[at] = now_p;
+      w.dst[at] = page;
       w.rows[at] = low % ps;
-      atomicSub(&c.ref[was], 1);
-      c.ref[now_p] = 1;
-      row[e] = now_p;
+      atomicSub(&ref.p[was], 1);
+      ref.p[page] = 1;
+      row[e] = page;
     }
-    for (int j = have + lane; j < max(np, pages_of(old, ps)); j += 32) {
-      const int p = j < np ? take[own + j - have] : -1;
+    for_row(take + mine - have, have, np, [&](int j, int p) {
       row[j] = p;
-      if (p >= 0) c.ref[p] = 1;
-    }
+      ref.p[p] = 1;
+    });
+    for (int j = np + lane; j < op; j += 32) row[j] = -1;
     __syncwarp();
-    if (lane == 0) c.len[s] = now;
+    if (lane == 0) c.len[s] = lens ? lens[i] : 0;
   }
+  __syncthreads();
+  close_counts(c, ref);
 }
 
 // mk_pages_fork, the same phases: give back what the destinations hold, count the partly
 // filled pages, rank free ones, share and write.
-__global__ void __launch_bounds__(kPlanThreads) plan_fork(mk_paged_cache c, const int* src, const int* dst, int n) {
-  __shared__ int red[32];
-  __shared__ long long red64[32];
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_fork(mk_paged_cache c, const int* src, const int* dst, int n) {
+  __shared__ Plan sm;
+  extern __shared__ __align__(16) int counts[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the copy kernel comes up meanwhile
   const Work w = work_of(c);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, ps = c.page_size;
+  const bool small = n <= kCached;
+  int* need = small ? sm.need : w.need;
+  auto get = [&](int i, int& a, int& b, int& len, int& had) {
+    if (small) {
+      a = sm.a[i], b = sm.own[i], len = sm.from[i], had = sm.to[i];
+    } else {
+      a = src[i], b = dst[i], len = c.len[a], had = c.len[b];
+    }
+  };
+  const Counts ref = open_counts(c, counts);
+  int* list = c.n_pages <= kListCached ? counts + ((c.n_pages + 3) & ~3) : w.list;
   if (tid == 0) w.count[0] = 0;
-  for (int i = tid; i < c.n_seqs; i += kPlanThreads) w.mark[i] = 0;
-  __syncthreads();
   int bad = 0;
   for (int i = tid; i < n; i += kPlanThreads) {
     const int a = src[i], b = dst[i];
-    if (a < 0 || a >= c.n_seqs || b < 0 || b >= c.n_seqs || atomicAdd(&w.mark[b], 1) || !len_ok(c, c.len[a]) ||
-        !len_ok(c, c.len[b]))
-      bad = 1;
+    const bool there = a >= 0 && a < c.n_seqs && b >= 0 && b < c.n_seqs;
+    const int len = there ? c.len[a] : 0, had = there ? c.len[b] : 0;
+    bad |= !there || !len_ok(c, len) || !len_ok(c, had);
+    if (there) w.mark[b] = i;
+    if (small) sm.a[i] = a, sm.own[i] = b, sm.from[i] = len, sm.to[i] = had;
+    need[i] = len % ps ? 1 : 0;
   }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) atomicOr(c.err, MK_DEVERR_BAD_PAGE);
-    return;
-  }
-  for (int i = warp; i < n; i += kPlanWarps) {
-    const int a = src[i], b = dst[i];
-    if (w.mark[a]) bad = 1;   // a source that is also a destination
-    const int* ra = c.table + static_cast<long long>(a) * c.max_pages;
-    const int* rb = c.table + static_cast<long long>(b) * c.max_pages;
-    for (int j = lane; j < pages_of(c.len[a], ps); j += 32)
-      if (ra[j] < 0 || ra[j] >= c.n_pages) bad = 1;
-    for (int j = lane; j < pages_of(c.len[b], ps); j += 32)
-      if (rb[j] < 0 || rb[j] >= c.n_pages) bad = 1;
-  }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) atomicOr(c.err, MK_DEVERR_BAD_PAGE);
-    return;
-  }
-  for (int i = warp; i < n; i += kPlanWarps) {
-    const int b = dst[i];
-    const int* rb = c.table + static_cast<long long>(b) * c.max_pages;
-    for (int j = lane; j < pages_of(c.len[b], ps); j += 32) atomicSub(&c.ref[rb[j]], 1);
-  }
-  for (int i = tid; i < n; i += kPlanThreads) w.need[i] = c.len[src[i]] % ps ? 1 : 0;
-  __syncthreads();
-  const int total = static_cast<int>(scan_need(w.need, n, red64));
-  if (list_free(c, total, w.list, red) < total) {
-    for (int i = warp; i < n; i += kPlanWarps) {
-      const int b = dst[i];
-      const int* rb = c.table + static_cast<long long>(b) * c.max_pages;
-      for (int j = lane; j < pages_of(c.len[b], ps); j += 32) atomicAdd(&c.ref[rb[j]], 1);
+  cp_async_wait<0>();
+  if (!__syncthreads_or(bad)) {
+    for (int i = tid; i < n; i += kPlanThreads) {
+      int a, b, len, had;
+      get(i, a, b, len, had);
+      // a source that is also a destination: its mark (which may be an old one) names a destination that is it
+      const int m = __ldcg(&w.mark[a]);
+      bad |= named_twice(w, b, i) || (m >= 0 && m < n && dst[m] == a);
     }
-    if (tid == 0) atomicOr(c.err, MK_DEVERR_NO_PAGES);
+    bad = __syncthreads_or(bad);
+  } else {
+    bad = 1;
+  }
+  if (bad) {
+    if (tid == 0) atomicOr(c.err, MK_DEVERR_BAD_PAGE);
     return;
   }
   for (int i = warp; i < n; i += kPlanWarps) {
-    const int a = src[i], b = dst[i], len = c.len[a], had = c.len[b], np = pages_of(len, ps);
-    const int* ra = c.table + static_cast<long long>(a) * c.max_pages;
+    int a, b, len, had;
+    get(i, a, b, len, had);
+    bad |= count_row(c, ref, b, 0, pages_of(had, ps), -1);
+    for_row(c.table + static_cast<long long>(a) * c.max_pages, 0, pages_of(len, ps),
+            [&](int, int p) { bad |= p < 0 || p >= c.n_pages; });
+  }
+  bad = __syncthreads_or(bad);
+  const int total = bad ? 0 : static_cast<int>(scan_need(need, n, sm.red));
+  if (bad || (ref.cached ? list_free<true>(ref, total, list, sm.red) : list_free<false>(ref, total, list, sm.red)) < total) {
+    for (int i = warp; i < n; i += kPlanWarps) {
+      int a, b, len, had;
+      get(i, a, b, len, had);
+      count_row(c, ref, b, 0, pages_of(had, ps), 1);
+    }
+    if (tid == 0) atomicOr(c.err, bad ? MK_DEVERR_BAD_PAGE : MK_DEVERR_NO_PAGES);
+    return;
+  }
+  for (int i = warp; i < n; i += kPlanWarps) {
+    int a, b, len, had;
+    get(i, a, b, len, had);
+    const int np = pages_of(len, ps);
     int* rb = c.table + static_cast<long long>(b) * c.max_pages;
-    for (int j = lane; j < max(np, pages_of(had, ps)); j += 32) {
-      int p = -1;
+    for_row(c.table + static_cast<long long>(a) * c.max_pages, 0, np, [&](int j, int p) {
       if (j < len / ps) {
-        p = ra[j];
-        atomicAdd(&c.ref[p], 1);
-      } else if (j < np) {
-        p = w.list[w.need[i]];
-        const int at = atomicAdd(&w.count[0], 1);
-        w.src[at] = ra[j];
-        w.dst[at] = p;
+        atomicAdd(&ref.p[p], 1);
+      } else {
+        const int page = list[need[i]], at = atomicAdd(&w.count[0], 1);
+        w.src[at] = p;
+        w.dst[at] = page;
         w.rows[at] = len % ps;
-        c.ref[p] = 1;
+        ref.p[page] = 1;
+        p = page;
       }
       rb[j] = p;
-    }
+    });
+    for (int j = np + lane; j < pages_of(had, ps); j += 32) rb[j] = -1;
     __syncwarp();
     if (lane == 0) c.len[b] = len;
   }
+  __syncthreads();
+  close_counts(c, ref);
 }
 
 // mk_pages_compact, counts and copies: pages in use, then the r-th used page with an id past
 // them paired with the r-th free id below (there are equally many). list[p] is the new id of
 // a moved page p; the table follows in remap_table.
-__global__ void __launch_bounds__(kPlanThreads) plan_compact(mk_paged_cache c) {
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_compact(mk_paged_cache c) {
   __shared__ int red[32];
   const Work w = work_of(c);
   const int tid = threadIdx.x;
@@ -332,7 +471,8 @@ struct CopyArgs {
 };
 constexpr int kCopyThreads = 256, kCopyPer = 8;
 
-__global__ void __launch_bounds__(kCopyThreads) copy_pages(CopyArgs a) {
+__global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant__ CopyArgs a) {
+  if (a.count) asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while its plan still runs
   const mk_paged_cache& f = a.from;
   const mk_paged_cache& t = a.to;
   const int count = a.count ? *a.count : a.n;
@@ -382,8 +522,16 @@ cudaError_t launch_copy(const CopyArgs& a, long long pairs, cudaStream_t s) {
   const long long vec = 2ll * a.from.n_layers * a.from.kv_heads * a.from.page_size * (a.from.head_dim / 8);
   const long long tasks = (vec + kCopyThreads * kCopyPer - 1) / (kCopyThreads * kCopyPer);
   const long long grid = std::min<long long>(148 * 4, tasks > (148 * 4) / std::max(1ll, pairs) ? 148 * 4 : tasks * pairs);
-  copy_pages<<<static_cast<int>(std::max(1ll, grid)), kCopyThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, grid)));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = a.count ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, copy_pages, a);
 }
 
 // The copies number the 16-byte vectors of a page in 32 bits.
@@ -401,6 +549,21 @@ int done(const char* who, cudaError_t e) {
   if (e == cudaSuccess) return MK_OK;
   mk_set_last_error(std::string(who) + ": " + cudaGetErrorString(e));
   return MK_ERR_CUDA;
+}
+
+using PlanKernel = void (*)(mk_paged_cache, const int*, const int*, int);
+cudaError_t launch_plan(PlanKernel kernel, const mk_paged_cache& c, const int* a, const int* b, int n, cudaStream_t s) {
+  static std::atomic<uint64_t> attr_set{0};   // per device, both kernels
+  const cudaError_t e = once_per_device(attr_set, [] {
+    const int bytes = kRefCached * static_cast<int>(sizeof(int));
+    const cudaError_t e1 = cudaFuncSetAttribute(plan_resize, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return e1 != cudaSuccess ? e1 : cudaFuncSetAttribute(plan_fork, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  });
+  if (e != cudaSuccess) return e;
+  const size_t counts = (static_cast<size_t>(c.n_pages) * sizeof(int) + 15) & ~size_t(15);
+  const size_t bytes = c.n_pages > kRefCached ? 0 : c.n_pages > kListCached ? counts : 2 * counts;
+  kernel<<<1, kPlanThreads, bytes, s>>>(c, a, b, n);
+  return cudaGetLastError();
 }
 
 cudaError_t copy_planned(const mk_paged_cache& c, long long pairs, cudaStream_t s) {
@@ -425,8 +588,7 @@ extern "C" int mk_pages_resize(const mk_paged_cache* c, const int32_t* d_seqs, c
   if (n == 0) return MK_OK;
   if (!d_seqs) return mk::refuse(who, "NULL sequence ids");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  mk::plan_resize<<<1, mk::kPlanThreads, 0, s>>>(*c, d_seqs, d_lens, n);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = mk::launch_plan(mk::plan_resize, *c, d_seqs, d_lens, n, s);
   if (e == cudaSuccess && d_lens) e = mk::copy_planned(*c, n, s);   // freeing replaces no page
   return mk::done(who, e);
 }
@@ -439,8 +601,7 @@ extern "C" int mk_pages_fork(const mk_paged_cache* c, const int32_t* d_src, cons
   if (n == 0) return MK_OK;
   if (!d_src || !d_dst) return mk::refuse(who, "NULL sequence ids");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  mk::plan_fork<<<1, mk::kPlanThreads, 0, s>>>(*c, d_src, d_dst, n);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = mk::launch_plan(mk::plan_fork, *c, d_src, d_dst, n, s);
   if (e == cudaSuccess) e = mk::copy_planned(*c, n, s);
   return mk::done(who, e);
 }

@@ -309,6 +309,38 @@ def test_random_page_operations(ps, n_pages, n_seqs, d, seed):
     assert p.len.sum() > 0
 
 
+def test_large_tables():
+    """More sequences in a call than a plan keeps in shared memory (1024) and more pages than it counts there
+    (49152): tables, lengths and counts against the loops."""
+    rng = random.Random(8)
+    c = hda().PagedCache.empty(1, 60001, 1, 8, 64, 1500, 40)
+    p = ref.Pages(60001, 1500, 40, 8)
+
+    def check(ok):
+        assert int(c.err.item()) == (0 if ok else hda().MK_DEVERR_NO_PAGES)
+        c.err.zero_()
+        for t, w in ((c.table, p.table), (c.len, p.len), (c.ref, p.ref)):
+            assert np.array_equal(t.cpu().numpy(), w)
+
+    def resize(ids, lens):
+        c.resize(ints(ids), ints(lens))
+        check(p.resize(ids, lens))
+
+    resize(list(range(1500)), [rng.randint(200, 320) for _ in range(1500)])   # past the 49152nd page
+    resize(list(range(1500)), [320] * 1500)
+    ids = rng.sample(range(1500), 1200)
+    resize(ids, [rng.randint(0, 320) for _ in ids])
+    dst = rng.sample(range(1500), 1100)
+    src = [rng.choice([i for i in range(1500) if i not in set(dst)]) for _ in range(3)]
+    src = [rng.choice(src) for _ in dst]
+    c.fork(ints(src), ints(dst))
+    check(p.fork(src, dst))
+    resize(dst[:1050], [rng.randint(0, 320) for _ in dst[:1050]])             # shared pages cut in the middle
+    c.compact()
+    p.compact()
+    check(True)
+
+
 def test_free_and_zero_lengths():
     c = hda().PagedCache.empty(1, 20, 1, 8, 64, 5, 4)
     c.resize(ints([4, 0, 2]), ints([32, 0, 9]))
