@@ -55,8 +55,15 @@ struct Lay {
   static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 6 : 8;
   static constexpr int kOffBars = kQ + kSlots * kSlot;
   static constexpr int kSmem = kOffBars + kBarBytes;
-  // TMEM columns: O [0, D), then two score buffers of 128, whose first 64 columns take P
+  // TMEM columns: O [0, D), then the score buffers of 128, whose first 64 columns take P. With three of
+  // them (head dims up to 128) the scores run two tiles ahead of the products, so a softmax group finds
+  // its next tile ready; 256 columns of O leave room for two.
   static constexpr uint32_t kColS = D;
+  static constexpr int kBufs = D == 256 ? 2 : 3, kAhead = kBufs - 1;
+  // Places of the n key and value tiles of a segment in the ring: the scores of kAhead + 1 tiles, the
+  // first product, and so on in turn, the last kAhead products at the end.
+  __device__ static int k_place(int j, int) { return j <= kAhead ? j : 2 * j - kAhead; }
+  __device__ static int v_place(int j, int n) { return j < n - kAhead ? 2 * j + kAhead + 1 : n + j; }
 };
 static_assert(Lay<256>::kSmem <= 232448 && Lay<128>::kSmem <= 232448, "fits the SM");
 
@@ -94,7 +101,7 @@ struct Segment {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], s_full[2], p_full[2], o_done[2], q_full, pair[4], m_full[2][4], seg_full[kSegs], seg_empty[kSegs];
+  uint64_t full[8], empty[8], s_full[3], p_full[3], o_done[2], q_full, pair[4], m_full[2][4], seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem;
   int abort;
   Segment seg[kSegs];
@@ -342,11 +349,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
       mbar_init(&b->full[i], 1);
       mbar_init(&b->empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&b->s_full[i], 1);
       mbar_init(&b->p_full[i], kSoftWarps / 2);
-      mbar_init(&b->o_done[i], 1);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&b->o_done[i], 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b->pair[i], 2);
       mbar_init(&b->m_full[0][i], 1);
@@ -359,7 +366,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
     }
     fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == 8) {   // (TMEM may still be the kernel's before on this SM: then this waits for its end)
     if (lane == 0) {
       tc::prefetch_tensormap(&tk);
       tc::prefetch_tensormap(&tv);
@@ -367,14 +374,18 @@ __global__ void __launch_bounds__(kThreads_, 1)
     tc::tmem_alloc(&b->tmem, 512);
     tc::tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // what came before in the stream is complete
   // units of every group of 32 sequences, one warp per group (in the ring's memory, before its first use)
   long long* groups = reinterpret_cast<long long*>(ring);
   const int n_groups = (a.w.n + 31) / 32;
-  for (int g = warp; g < n_groups; g += kThreads_ / 32) {
+  SeqWork first{};           // the scheduler's warp keeps the first group
+  long long first_units = 0;
+  for (int g = (warp + kThreads_ / 32 - 10) % (kThreads_ / 32); g < n_groups; g += kThreads_ / 32) {
     int bad = 0;
     const SeqWork w = seq_work(a, g * 32 + lane, &bad);
-    const long long u = warp_sum64(head_units(a, w)) * a.c.kv_heads;
+    const long long hu = head_units(a, w), u = warp_sum64(hu) * a.c.kv_heads;
     if (lane == 0) groups[g] = u;
+    if (g == 0) first = w, first_units = hu;
     if (bad && blockIdx.x == 0) atomicOr(err, MK_DEVERR_BAD_PAGE);
   }
   tc::fence_before_sync();
@@ -417,8 +428,8 @@ __global__ void __launch_bounds__(kThreads_, 1)
     long long u = u0;
     for (; u < u1 && ok && g < n_groups; ++g) {
       int bad = 0;
-      const SeqWork mine = seq_work(a, g * 32 + lane, &bad);
-      const long long hu = head_units(a, mine), units = hu * a.c.kv_heads;
+      const SeqWork mine = g ? seq_work(a, g * 32 + lane, &bad) : first;
+      const long long hu = g ? head_units(a, mine) : first_units, units = hu * a.c.kv_heads;
       const long long incl = before + warp_scan64(units);
       while (ok && u < u1) {
         const unsigned past = __ballot_sync(0xFFFFFFFFu, incl > u);
@@ -501,9 +512,9 @@ __global__ void __launch_bounds__(kThreads_, 1)
         }
         const int boxes = min(per_tile, (s.len - t * kN + a.box - 1) / a.box);   // up to the sequence's end
         const int y = (t * kN + lane * a.box) % a.c.page_size;                   // a box never crosses a page
-        // place of the tile in the order K0 K1 V0 K2 V1 ... (the ring's releases come in this order too, and a
-        // producer is never more than kSlots past its last wait, so no phase is skipped)
-        const uint32_t at = base + L::kCh * (is_v ? (j < n - 1 ? 2 * j + 2 : 2 * n - 1) : j ? 2 * j - 1 : 0);
+        // the ring's releases come in the order of its slots too, and a producer is never more than kSlots
+        // past its last wait, so no phase is skipped
+        const uint32_t at = base + L::kCh * (is_v ? L::v_place(j, n) : L::k_place(j, n));
         for (int c = 0; c < L::kCh && ok; ++c) {
           const uint32_t slot = at + c, k = slot % L::kSlots;
           if (slot >= L::kSlots) ok = warp_wait(b, &b->empty[k], (slot / L::kSlots - 1) & 1, err);
@@ -544,8 +555,9 @@ __global__ void __launch_bounds__(kThreads_, 1)
       commit(&b->empty[k], issue);
       if (++k == L::kSlots) k = 0, phase ^= 1;
     };
-    auto scores = [&](uint32_t n) {                // S buffer n & 1; its P was consumed by the product before
-      const uint32_t d = tmem + L::kColS + (n & 1) * kN;
+    uint32_t sbuf = 0, pbuf = 0, pphase = 0;       // score buffer of the next scores; of the next product, and its phase
+    auto scores = [&] {                            // the buffer's P was consumed by a product issued before
+      const uint32_t d = tmem + L::kColS + sbuf * kN;
 #pragma unroll
       for (int c = 0; c < L::kCh; ++c) {
         if (!take()) return;
@@ -558,7 +570,8 @@ __global__ void __launch_bounds__(kThreads_, 1)
                    (c | p | kk) ? 1u : 0u, issue);
         pass();
       }
-      commit(&b->s_full[n & 1], issue);
+      commit(&b->s_full[sbuf], issue);
+      sbuf = sbuf == L::kBufs - 1 ? 0 : sbuf + 1;
     };
     for (int i = 0; ok; ++i) {
       if (!warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) break;
@@ -569,11 +582,12 @@ __global__ void __launch_bounds__(kThreads_, 1)
       if (len == 0) continue;
       if (!(ok = warp_wait(b, &b->q_full, nq++ & 1, err))) break;
       tc::fence_after_sync();
-      scores(it);
+      for (int t = 0; t < L::kAhead && t < n; ++t) scores();
       for (int t = 0; t < n && ok; ++t, ++it) {
-        if (t + 1 < n) scores(it + 1);
-        if (!ok || !(ok = warp_wait(b, &b->p_full[it & 1], (it >> 1) & 1, err))) break;
-        const uint32_t pa = tmem + L::kColS + (it & 1) * kN, more = t > 0;
+        if (t + L::kAhead < n) scores();
+        if (!ok || !(ok = warp_wait(b, &b->p_full[pbuf], pphase, err))) break;
+        const uint32_t pa = tmem + L::kColS + pbuf * kN, more = t > 0;
+        if (++pbuf == L::kBufs) pbuf = 0, pphase ^= 1;
 #pragma unroll
         for (int c = 0; c < L::kCh; ++c) {
           if (!take()) break;
@@ -596,7 +610,6 @@ __global__ void __launch_bounds__(kThreads_, 1)
     // memory (published before the exponentials); each group keeps its own l.
     const int quarter = warp & 3, grp = warp >> 2, r = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t sb = tmem + lanes + L::kColS + grp * kN;
     uint32_t it = 0, slot = 0, meets = 0;
     Segment s;
     // the next segment, and its row tile's queries on their way into the swizzled layout (whose last
@@ -636,9 +649,10 @@ __global__ void __launch_bounds__(kThreads_, 1)
       for (int j = 0; j < n; ++j, ++it) {
         if ((it & 1) != static_cast<uint32_t>(grp)) continue;
         const int t = s.t0 + j;
-        if (!(ok = warp_wait(b, &b->s_full[grp], (it >> 1) & 1, err))) break;
-        // long done (issued before these scores), but a parity wait must not skip a phase
-        if (it >= 2 && !(ok = warp_wait(b, &b->o_done[grp], ((it >> 1) - 1) & 1, err))) break;
+        const uint32_t buf = it % L::kBufs, sb = tmem + lanes + L::kColS + buf * kN;
+        // (of the tiles that had this buffer before, the last one's scores are complete: they were issued before
+        // those of this group's last tile, so no phase is skipped)
+        if (!(ok = warp_wait(b, &b->s_full[buf], (it / L::kBufs) & 1, err))) break;
         if (live) {
           tc::fence_after_sync();
           const int key0 = t * kN;
@@ -720,7 +734,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
         }
         if ((t + 1) * kN > s.len) {
           // positions from len on: whatever lies there must not meet a weight of zero as NaN
-          const uint32_t at = slot + L::kCh * (j < n - 1 ? 2 * j + 2 : 2 * n - 1);
+          const uint32_t at = slot + L::kCh * L::v_place(j, n);
           for (int c = 0; c < L::kCh && ok; ++c) {
             const uint32_t k = (at + c) % L::kSlots;
             ok = warp_wait(b, &b->full[k], ((at + c) / L::kSlots) & 1, err);
@@ -734,9 +748,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
           if (!ok) break;
           tc::fence_proxy_async_smem();
         }
+        // this group's product before is done by now, but a parity wait must not skip a phase
+        if (it >= 2 && !(ok = warp_wait(b, &b->o_done[grp], ((it >> 1) - 1) & 1, err))) break;
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->p_full[grp]);
+        if (lane == 0) mbar_arrive(&b->p_full[buf]);
       }
       if (!ok) break;
       slot += 2u * L::kCh * n;
@@ -745,7 +761,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
       const int part = s.part;
       const int h = s.kvh * a.group + rr0 + min(r, rows - 1) - tok * a.group;
       uint16_t* out = a.o + static_cast<long long>(s.row0 + tok) * a.ldo + static_cast<long long>(h) * D;
-      if (n > 0 && !(ok = warp_wait(b, &b->s_full[(it - 1) & 1], ((it - 1) >> 1) & 1, err))) break;
+      if (n > 0 && !(ok = warp_wait(b, &b->s_full[(it - 1) % L::kBufs], ((it - 1) / L::kBufs) & 1, err))) break;
       if (!(ok = fetch(++i))) break;
       float m = -INFINITY;
       if (n > 0) {
@@ -811,6 +827,7 @@ __global__ void __launch_bounds__(256) join_parts(const __grid_constant__ AttnAr
   constexpr int E = D / 32;
   __shared__ float so[8][D];
   __shared__ float2 sm[8];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lead = blockIdx.x;
   const int* meta = a.meta + static_cast<long long>(lead) * kMeta;
@@ -883,18 +900,22 @@ cudaError_t launch_attn(const CUtensorMap& tk, const CUtensorMap& tv, const Attn
     return cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  paged_attn_kernel<D><<<grid, kThreads_, Lay<D>::kSmem, s>>>(tk, tv, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // both kernels come up while the one before them in the stream drains, and wait for it themselves
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * grid, std::min(kJoinY, a.max_rows));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
   cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;   // launched while the first kernel drains
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  cfg.stream = s;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads_);
+  cfg.dynamicSmemBytes = Lay<D>::kSmem;
+  e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D>, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(2 * grid, std::min(kJoinY, a.max_rows));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_parts<D>, a, 2 * grid);
 }
 
