@@ -106,6 +106,7 @@ struct Bars {
   int abort;
   Segment seg[kSegs];
   float m[2][kM], l[2][kM];   // [softmax group][row]
+  int pages[2][2][16];        // [keys, values][tile parity][box]: page of each box of a tile
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barriers fit their slot");
 
@@ -482,8 +483,9 @@ __global__ void __launch_bounds__(kThreads_, 1)
     stop.end = 1;
     if (ok) emit(stop);
   } else if (warp == 8 || warp == 11) {
-    // ---- TMA producers, of the keys and of the values. Lane i loads box i of a tile: its page is read
-    // two tiles ahead and checked one tile ahead of the load that uses it.
+    // ---- TMA producers, of the keys and of the values. Lane i reads the page of box i of a tile two tiles
+    // ahead of its use; one elected lane issues the loads (a load issued by each lane in turn cost
+    // about 110 clocks a box).
     const bool is_v = warp == 11;
     const CUtensorMap* map = is_v ? &tv : &tk;
     const int per_tile = kN / a.box;
@@ -511,7 +513,10 @@ __global__ void __launch_bounds__(kThreads_, 1)
           now = a.c.n_pages;                       // outside the tensor map: reads as zeros
         }
         const int boxes = min(per_tile, (s.len - t * kN + a.box - 1) / a.box);   // up to the sequence's end
-        const int y = (t * kN + lane * a.box) % a.c.page_size;                   // a box never crosses a page
+        const int y0 = t * kN % a.c.page_size;                                   // a box never crosses a page
+        int* pages = b->pages[is_v][j & 1];
+        if (lane < per_tile) pages[lane] = now;
+        __syncwarp();
         // the ring's releases come in the order of its slots too, and a producer is never more than kSlots
         // past its last wait, so no phase is skipped
         const uint32_t at = base + L::kCh * (is_v ? L::v_place(j, n) : L::k_place(j, n));
@@ -519,13 +524,19 @@ __global__ void __launch_bounds__(kThreads_, 1)
           const uint32_t slot = at + c, k = slot % L::kSlots;
           if (slot >= L::kSlots) ok = warp_wait(b, &b->empty[k], (slot / L::kSlots - 1) & 1, err);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&b->full[k], boxes * a.box * L::kCW * 2);
-          __syncwarp();
-          if (lane < boxes) {
+          if (elect_lane()) {
+            mbar_arrive_expect_tx(&b->full[k], boxes * a.box * L::kCW * 2);
+            uint8_t* to = ring + k * L::kSlot;
+            int y = y0;
+            for (int i = 0; i < boxes; ++i, to += a.box * 128) {
+              const int w = pages[i];
 #pragma unroll
-            for (int p = 0; p < L::kCW / 64; ++p)
-              tma_box(ring + k * L::kSlot + p * kPanel + lane * a.box * 128, map, c * L::kCW + p * 64, y, s.kvh, now, &b->full[k]);
+              for (int p = 0; p < L::kCW / 64; ++p) tma_box(to + p * kPanel, map, c * L::kCW + p * 64, y, s.kvh, w, &b->full[k]);
+              y += a.box;
+              if (y == a.c.page_size) y = 0;
+            }
           }
+          __syncwarp();
           last = slot + 1;
         }
         now = next;
