@@ -1,8 +1,8 @@
 // Causal attention of new tokens over the pages of a KV cache, on the sm_100a tensor cores.
 //
-// The query heads that share a kv head are packed: row rr of a sequence and kv head is token
-// rr / group, head kv_head * group + rr % group, so one pass over the keys serves the whole group. A tile
-// is 128 such rows against 128 keys, and a work unit is one (row tile, key tile). All units of a call,
+// The query heads that share a kv head are packed: a row tile is 128 / group tokens times the group's
+// heads (row r: token r / group, head kv_head * group + r % group), so one pass over the keys serves the whole
+// group. A work unit is one row tile against one key tile of 128 keys. All units of a call,
 // in the order sequence, kv head, row tile, key tile, are cut into one equal run per CTA (one CTA
 // per SM), so a single long sequence spreads over the whole GPU and ragged ones balance; a row
 // tile whose key range is cut leaves partial results (O, m, l), which a second kernel joins.
@@ -10,7 +10,7 @@
 // Per key tile, with the scores in log2 units (c = scale log2 e):
 //   S = Q K^T                         tcgen05, M = 128, N = 128, K = D, into TMEM
 //   m = max(m, rowmax(c S));  P = 2^(c S - m), masked above the diagonal;  l += rowsum(P)
-//   O = O + P V                       tcgen05, P (bf16) read from TMEM over the columns of S
+//   O = O + P V                       tcgen05, P (bf16) read from TMEM
 // m is only raised (and O, l rescaled) when a tile's maximum passes it by more than 2^8, so
 // weights are at most 2^8 and the result O / l is the same softmax. m, l, S, O and the partial results
 // are fp32; a weight is rounded to bf16 once, as an operand, and the result once, at the end.
@@ -40,7 +40,6 @@ constexpr int kM = 128, kN = 128;        // rows and keys of a tile
 constexpr int kSoftWarps = 8;
 constexpr int kThreads_ = 384;
 constexpr int kSegs = 4;                 // segments the scheduler runs ahead
-constexpr int kOver = 2;                 // what a row tile costs beside its key tiles (queries in, results out), in key tiles
 constexpr float kRaise = 8.0f;           // log2 units
 constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int kPanel = 128 * 128;        // 64 bf16 entries of 128 rows: 16 KB
@@ -55,11 +54,12 @@ struct Lay {
   static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 6 : 8;
   static constexpr int kOffBars = kQ + kSlots * kSlot;
   static constexpr int kSmem = kOffBars + kBarBytes;
-  // TMEM columns: O [0, D), then the score buffers of 128, whose first 64 columns take P. With three of
-  // them (head dims up to 128) the scores run two tiles ahead of the products, so a softmax group finds
-  // its next tile ready; 256 columns of O leave room for two.
-  static constexpr uint32_t kColS = D;
-  static constexpr int kBufs = D == 256 ? 2 : 3, kAhead = kBufs - 1;
+  // TMEM columns: O [0, D), score buffers of 128 columns, two P buffers of 64. A softmax group holds its
+  // tile's scores in registers, so the next scores overwrite them as soon as they are loaded, and the chain
+  // from one tile of a group to its next is the softmax alone. 256 columns of O leave room
+  // for one score buffer, smaller ones for two, and the scores run that many tiles ahead of the products.
+  static constexpr int kBufs = D == 256 ? 1 : 2, kAhead = kBufs;
+  static constexpr uint32_t kColS = D, kColP = D + kBufs * 128;
   // Places of the n key and value tiles of a segment in the ring: the scores of kAhead + 1 tiles, the
   // first product, and so on in turn, the last kAhead products at the end.
   __device__ static int k_place(int j, int) { return j <= kAhead ? j : 2 * j - kAhead; }
@@ -74,6 +74,8 @@ struct AttnArgs {
   long long ldq;
   uint16_t* o;
   long long ldo;
+  int tokens, few;         // of a row tile: 128 / group; of the smaller box of queries
+  int over;                // key tiles that a full row tile's queries and results cost, beside one
   float c2;                // |scale| log2 e
   int negative;            // the sign of scale
   NewRows w;
@@ -101,7 +103,7 @@ struct Segment {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], s_full[3], p_full[3], o_done[2], q_full, pair[4], m_full[2][4], seg_full[kSegs], seg_empty[kSegs];
+  uint64_t full[8], empty[8], s_full[2], s_free[2], p_full[2], o_done[2], q_full, q_free, pair[4], m_full[2][4], seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem;
   int abort;
   Segment seg[kSegs];
@@ -199,19 +201,40 @@ __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
       : "memory");
 }
-// 32 bytes to a 32-byte aligned address: one store, so that a lane's row takes a whole sector.
-__device__ __forceinline__ void store32(void* p, const uint32_t* u) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]),
-               "r"(u[5]), "r"(u[6]), "r"(u[7])
-               : "memory");
+__device__ __forceinline__ void tma_box3(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
 }
-// The same to a 16-byte aligned address (a row pitch may be an odd multiple of 8 entries).
-__device__ __forceinline__ void store_bf16x16(uint16_t* p, const uint32_t* u) {
-  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
-    store32(p, u);
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+// Each lane has 128 bytes of its row r at p (32 registers, 8 pieces of 16 bytes); rows from `rows` on are not
+// written. The pieces are transposed within groups of 8 lanes (three exchanges of halves), the addresses with them.
+__device__ __forceinline__ void store_rows(void* p, uint32_t* u, int r, int rows) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 4; s >= 1; s /= 2) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k & s) continue;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t &lo = u[4 * k + c], &hi = u[4 * (k + s) + c];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, s);
+        if (up)
+          lo = got;
+        else
+          hi = got;
+      }
+    }
+  }
+  const long long at = reinterpret_cast<long long>(p);
+  const int first = r - (lane & 7);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const long long to = __shfl_sync(0xFFFFFFFFu, at, (lane & ~7) + k) + (lane & 7) * 16;
+    if (first + k < rows) *reinterpret_cast<uint4*>(to) = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
   }
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -287,14 +310,18 @@ __device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int i, int* bad) 
   w.seq = there ? s : 0;
   w.len = ok ? len : 0;
   w.pos0 = w.len - (e - w.row0);
-  w.row_tiles = (w.rows * a.group + kM - 1) / kM;   // below 2^30 (checked by the host)
+  w.row_tiles = (w.rows + a.tokens - 1) / a.tokens;
   return w;
 }
 // Key tiles of row tile j: up to the position of its last row; one (empty) where it sees nothing.
 __device__ __forceinline__ int key_tiles(const AttnArgs& a, const SeqWork& w, int j) {
-  const int last = min((j + 1) * kM, w.rows * a.group) - 1;
-  const int keys = w.pos0 + last / a.group + 1;
+  const int keys = w.pos0 + min((j + 1) * a.tokens, w.rows);
   return max(1, (keys + kN - 1) / kN);
+}
+// What row tile j costs beside its key tiles, in units of them: measured at about 3 key tiles for 128 rows
+// of 256 entries and 6 of 128 (the products of 256 take twice as long), next to nothing for a few rows.
+__device__ __forceinline__ int extra_units(const AttnArgs& a, const SeqWork& w, int j) {
+  return 1 + min(a.tokens, w.rows - j * a.tokens) * a.group * a.over / kM;
 }
 __device__ __forceinline__ SeqWork shfl_work(const SeqWork& w, int src) {
   return SeqWork{__shfl_sync(0xFFFFFFFFu, w.row0, src), __shfl_sync(0xFFFFFFFFu, w.rows, src), __shfl_sync(0xFFFFFFFFu, w.pos0, src),
@@ -305,12 +332,12 @@ __device__ long long head_units(const AttnArgs& a, const SeqWork& w) {
   const int lane = threadIdx.x & 31;
   long long u = 0;
   if (w.row_tiles <= 4)
-    for (int j = 0; j < w.row_tiles; ++j) u += kOver + key_tiles(a, w, j);
+    for (int j = 0; j < w.row_tiles; ++j) u += extra_units(a, w, j) + key_tiles(a, w, j);
   for (unsigned big = __ballot_sync(0xFFFFFFFFu, w.row_tiles > 4); big; big &= big - 1) {
     const int src = __ffs(big) - 1;
     const SeqWork x = shfl_work(w, src);
     int sum = 0;
-    for (int j = lane; j < x.row_tiles; j += 32) sum += kOver + key_tiles(a, x, j);
+    for (int j = lane; j < x.row_tiles; j += 32) sum += extra_units(a, x, j) + key_tiles(a, x, j);
     const int t = __reduce_add_sync(0xFFFFFFFFu, sum);
     if (lane == src) u = t;
   }
@@ -332,7 +359,8 @@ __device__ __forceinline__ long long warp_scan64(long long v) {   // inclusive
 
 template <int D>
 __global__ void __launch_bounds__(kThreads_, 1)
-    paged_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const __grid_constant__ AttnArgs a) {
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tq1, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                      const __grid_constant__ AttnArgs a) {
   using L = Lay<D>;
   extern __shared__ __align__(1024) uint8_t smem[];   // swizzled tiles need 1024-byte alignment
   uint8_t* ring = smem + L::kQ;
@@ -350,17 +378,19 @@ __global__ void __launch_bounds__(kThreads_, 1)
       mbar_init(&b->full[i], 1);
       mbar_init(&b->empty[i], 1);
     }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 2; ++i) {              // by tile parity: each is one softmax group's
       mbar_init(&b->s_full[i], 1);
+      mbar_init(&b->s_free[i], kSoftWarps / 2);
       mbar_init(&b->p_full[i], kSoftWarps / 2);
+      mbar_init(&b->o_done[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&b->o_done[i], 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b->pair[i], 2);
       mbar_init(&b->m_full[0][i], 1);
       mbar_init(&b->m_full[1][i], 1);
     }
-    mbar_init(&b->q_full, kSoftWarps);
+    mbar_init(&b->q_full, 1);
+    mbar_init(&b->q_free, 1);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&b->seg_full[i], 1);
       mbar_init(&b->seg_empty[i], kSoftWarps + 3);
@@ -369,6 +399,8 @@ __global__ void __launch_bounds__(kThreads_, 1)
   }
   if (warp == 8) {   // (TMEM may still be the kernel's before on this SM: then this waits for its end)
     if (lane == 0) {
+      tc::prefetch_tensormap(&tq);
+      tc::prefetch_tensormap(&tq1);
       tc::prefetch_tensormap(&tk);
       tc::prefetch_tensormap(&tv);
     }
@@ -412,7 +444,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
   asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == 10) {
     // ---- scheduler: cut [u0, u1) into segments
-    int emitted = 0, made = 0;
+    int emitted = 0, made = 0, with_queries = 0;
     bool ok = true;
     auto emit = [&](const Segment& s) {
       const int k = emitted % kSegs;
@@ -423,6 +455,20 @@ __global__ void __launch_bounds__(kThreads_, 1)
         mbar_arrive(&b->seg_full[k]);
       }
       ++emitted;
+      if (s.end || s.len == 0) return;
+      // its queries, once the last scores of the row tile before are computed: boxes of 64 entries x group heads x
+      // tokens, which is the packed order (rows past the sequence are another's, or zeros, and are not used)
+      if (with_queries && !(ok = warp_wait(b, &b->q_free, (with_queries - 1) & 1, err))) return;
+      ++with_queries;
+      if (elect_lane()) {
+        // the smaller box where it holds all (decode): the whole one would be mostly other rows
+        const bool few = s.new_rows - s.tile * a.tokens <= a.few;
+        mbar_arrive_expect_tx(&b->q_full, (few ? a.few : a.tokens) * a.group * D * 2);
+#pragma unroll
+        for (int p = 0; p < D / 64; ++p)
+          tma_box3(smem + p * kPanel, few ? &tq1 : &tq, p * 64, s.kvh * a.group, s.row0 + s.tile * a.tokens, &b->q_full);
+      }
+      __syncwarp();
     };
     for (int k = lane; k < 2 * kMeta; k += 32) a.meta[blockIdx.x * 2 * kMeta + k] = 0;
     __syncwarp();
@@ -444,7 +490,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
         s.kvh = static_cast<int>(rel / h);
         int rem = static_cast<int>(rel - s.kvh * h), tiles = 0;
         for (int j0 = 0;; j0 += 32) {              // the row tile that holds unit rem of this head
-          const int t = j0 + lane < w.row_tiles ? kOver + key_tiles(a, w, j0 + lane) : 0;
+          const int t = j0 + lane < w.row_tiles ? extra_units(a, w, j0 + lane) + key_tiles(a, w, j0 + lane) : 0;
           const int inc = static_cast<int>(warp_scan64(t));
           const unsigned hit = __ballot_sync(0xFFFFFFFFu, inc > rem);
           if (hit) {
@@ -456,21 +502,22 @@ __global__ void __launch_bounds__(kThreads_, 1)
           }
           rem -= __shfl_sync(0xFFFFFFFFu, inc, 31);
         }
-        // tiles counts kOver units and then the key tiles; a run that ends in the former leaves the
+        // tiles counts the extra units and then the key tiles; a run that ends in the former leaves the
         // row tile to the next CTA
+        const int over = extra_units(a, w, s.tile);
         const int upto = static_cast<int>(min(static_cast<long long>(tiles), rem + (u1 - u)));
         u += upto - rem;
-        s.t0 = max(0, rem - kOver);
-        s.t1 = upto - kOver;
+        s.t0 = max(0, rem - over);
+        s.t1 = upto - over;
         if (s.t1 <= s.t0) continue;
-        tiles -= kOver;
+        tiles -= over;
         const bool whole = s.t0 == 0 && s.t1 == tiles;
         s.part = whole ? -1 : static_cast<int>(blockIdx.x) * 2 + (made ? 1 : 0);
         ++made;
         if (!whole && lane == 0) {
           int* m = a.meta + static_cast<long long>(s.part) * kMeta;
           m[0] = kPartUsed | (s.t0 == 0 ? kPartFirst : 0) | (s.t1 == tiles ? kPartLast : 0);
-          m[1] = min(kM, w.rows * a.group - s.tile * kM);
+          m[1] = min(a.tokens, w.rows - s.tile * a.tokens) * a.group;
           m[2] = s.tile;
           m[3] = s.kvh;
           m[4] = s.row0;
@@ -482,6 +529,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
     Segment stop{};
     stop.end = 1;
     if (ok) emit(stop);
+    if (!ok && with_queries && lane == 0) {        // queries in flight land before the CTA ends (bounded)
+      int never = 0;
+      mbar_wait(&b->q_full, (with_queries - 1) & 1, &never, kWaitNs / 10);
+    }
+    __syncwarp();
   } else if (warp == 8 || warp == 11) {
     // ---- TMA producers, of the keys and of the values. Lane i reads the page of box i of a tile two tiles
     // ahead of its use; one elected lane issues the loads (a load issued by each lane in turn cost
@@ -566,9 +618,14 @@ __global__ void __launch_bounds__(kThreads_, 1)
       commit(&b->empty[k], issue);
       if (++k == L::kSlots) k = 0, phase ^= 1;
     };
-    uint32_t sbuf = 0, pbuf = 0, pphase = 0;       // score buffer of the next scores; of the next product, and its phase
-    auto scores = [&] {                            // the buffer's P was consumed by a product issued before
-      const uint32_t d = tmem + L::kColS + sbuf * kN;
+    uint32_t ahead = 0;                            // tiles whose scores were issued
+    auto scores = [&] {
+      const uint32_t d = tmem + L::kColS + ahead % L::kBufs * kN;
+      if (ahead >= L::kBufs) {                     // the buffer's last scores are in registers
+        const uint32_t was = ahead - L::kBufs;
+        if (!(ok = ok && warp_wait(b, &b->s_free[was & 1], (was >> 1) & 1, err))) return;
+        tc::fence_after_sync();
+      }
 #pragma unroll
       for (int c = 0; c < L::kCh; ++c) {
         if (!take()) return;
@@ -581,8 +638,8 @@ __global__ void __launch_bounds__(kThreads_, 1)
                    (c | p | kk) ? 1u : 0u, issue);
         pass();
       }
-      commit(&b->s_full[sbuf], issue);
-      sbuf = sbuf == L::kBufs - 1 ? 0 : sbuf + 1;
+      commit(&b->s_full[ahead & 1], issue);
+      ++ahead;
     };
     for (int i = 0; ok; ++i) {
       if (!warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) break;
@@ -594,11 +651,14 @@ __global__ void __launch_bounds__(kThreads_, 1)
       if (!(ok = warp_wait(b, &b->q_full, nq++ & 1, err))) break;
       tc::fence_after_sync();
       for (int t = 0; t < L::kAhead && t < n; ++t) scores();
+      if (n <= L::kAhead) commit(&b->q_free, issue);
       for (int t = 0; t < n && ok; ++t, ++it) {
-        if (t + L::kAhead < n) scores();
-        if (!ok || !(ok = warp_wait(b, &b->p_full[pbuf], pphase, err))) break;
-        const uint32_t pa = tmem + L::kColS + pbuf * kN, more = t > 0;
-        if (++pbuf == L::kBufs) pbuf = 0, pphase ^= 1;
+        if (t + L::kAhead < n) {
+          scores();
+          if (t + L::kAhead == n - 1) commit(&b->q_free, issue);
+        }
+        if (!ok || !(ok = warp_wait(b, &b->p_full[it & 1], (it >> 1) & 1, err))) break;
+        const uint32_t pa = tmem + L::kColP + (it & 1) * (kN / 2), more = t > 0;
 #pragma unroll
         for (int c = 0; c < L::kCh; ++c) {
           if (!take()) break;
@@ -623,47 +683,26 @@ __global__ void __launch_bounds__(kThreads_, 1)
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     uint32_t it = 0, slot = 0, meets = 0;
     Segment s;
-    // the next segment, and its row tile's queries on their way into the swizzled layout (whose last
-    // reader, the row tile before, has computed its scores)
+    const int tok = r / a.group, head = r - tok * a.group;   // of this row in every row tile
+    const int first_tok = quarter * 32 / a.group;            // of the warp's first row
     auto fetch = [&](int i) {
       if (!warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) return false;
       s = b->seg[i % kSegs];
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->seg_empty[i % kSegs]);
-      if (s.end || s.len == 0) return true;
-      constexpr int kLanes = D / 8, kAtOnce = kSoftWarps * 32 / kLanes;   // lanes of a row, rows at once
-      const int rows = min(kM, s.new_rows * a.group - s.tile * kM), e = threadIdx.x % kLanes;
-      for (int row = threadIdx.x / kLanes; row < rows; row += kAtOnce) {
-        const int rr = s.tile * kM + row, tok = rr / a.group, h = s.kvh * a.group + rr - tok * a.group;
-        cp_async16(smem + (e >> 3) * kPanel + row * 128 + (((e & 7) ^ (row & 7)) << 4),
-                   a.q + static_cast<long long>(s.row0 + tok) * a.ldq + h * D + e * 8, 16);
-      }
-      cp_async_commit();
       return true;
     };
-    auto queries_in = [&] {
-      if (s.end || s.len == 0) return;
-      cp_async_wait<0>();
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b->q_full);
-    };
     bool ok = fetch(0);
-    if (ok) queries_in();
     for (int i = 0; ok && !s.end;) {
-      const int rr0 = s.tile * kM, rows = min(kM, s.new_rows * a.group - rr0);
+      const int tok0 = s.tile * a.tokens, rows = min(a.tokens, s.new_rows - tok0) * a.group;
       const bool live = quarter * 32 < rows;       // the warp has rows of the tile
-      const int tok = (rr0 + min(r, rows - 1)) / a.group, pos = s.pos0 + tok;
-      const int pos_first = s.pos0 + (rr0 + quarter * 32) / a.group;   // the warp's lowest
+      const int pos = s.pos0 + tok0 + tok, pos_first = s.pos0 + tok0 + first_tok;   // the row's, and the warp's lowest
       const int n = s.len == 0 ? 0 : s.t1 - s.t0;
       float l = 0.f, ml = -INFINITY;               // this group's sum, and the m (log2 units) it goes by
       for (int j = 0; j < n; ++j, ++it) {
         if ((it & 1) != static_cast<uint32_t>(grp)) continue;
         const int t = s.t0 + j;
-        const uint32_t buf = it % L::kBufs, sb = tmem + lanes + L::kColS + buf * kN;
-        // (of the tiles that had this buffer before, the last one's scores are complete: they were issued before
-        // those of this group's last tile, so no phase is skipped)
-        if (!(ok = warp_wait(b, &b->s_full[buf], (it / L::kBufs) & 1, err))) break;
+        if (!(ok = warp_wait(b, &b->s_full[grp], (it >> 1) & 1, err))) break;
         if (live) {
           tc::fence_after_sync();
           const int key0 = t * kN;
@@ -671,9 +710,12 @@ __global__ void __launch_bounds__(kThreads_, 1)
           // the row's 128 scores stay in registers: four loads in flight, and one pass for the maximum
           float x[kN];
 #pragma unroll
-          for (int c = 0; c < kN; c += 32) tmem_ld32(sb + c, x + c);
+          for (int c = 0; c < kN; c += 32) tmem_ld32(tmem + lanes + L::kColS + it % L::kBufs * kN + c, x + c);
 #pragma unroll
           for (int c = 0; c < kN; c += 32) tmem_wait_ld(x + c);
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b->s_free[grp]);
           if (a.negative) {
 #pragma unroll
             for (int c = 0; c < kN; ++c) x[c] = -x[c];
@@ -718,6 +760,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
             }
             tmem_wait_st();
           }
+          // P's columns are free once this group's product before is done (it was its own wait's phase)
+          if (it >= 2) {
+            if (!(ok = warp_wait(b, &b->o_done[grp], ((it >> 1) - 1) & 1, err))) break;
+            tc::fence_after_sync();
+          }
           if (ml != m) l *= ex2(ml - m);           // m may have been raised at the other group's tile
           ml = m;
           const float sub = m == -INFINITY ? 0.f : -m;
@@ -736,12 +783,16 @@ __global__ void __launch_bounds__(kThreads_, 1)
               p[k] = pack_bf16(p0, p1);
               p[k + 1] = pack_bf16(p2, p3);
             }
-            tmem_st16(sb + c / 2, p);              // over the scores, which have all been loaded
+            tmem_st16(tmem + lanes + L::kColP + grp * (kN / 2) + c / 2, p);
           }
           tmem_wait_st();
           l += f2_sum(add2(sum0, sum1));
-        } else if (lane == 0) {
-          mbar_arrive(&b->m_full[grp][quarter]);   // nothing to pass on, but the phases count tiles
+        } else {
+          if (lane == 0) {                         // nothing to load or to pass on, but the phases count tiles
+            mbar_arrive(&b->s_free[grp]);
+            mbar_arrive(&b->m_full[grp][quarter]);
+          }
+          if (it >= 2 && !(ok = warp_wait(b, &b->o_done[grp], ((it >> 1) - 1) & 1, err))) break;
         }
         if ((t + 1) * kN > s.len) {
           // positions from len on: whatever lies there must not meet a weight of zero as NaN
@@ -759,20 +810,15 @@ __global__ void __launch_bounds__(kThreads_, 1)
           if (!ok) break;
           tc::fence_proxy_async_smem();
         }
-        // this group's product before is done by now, but a parity wait must not skip a phase
-        if (it >= 2 && !(ok = warp_wait(b, &b->o_done[grp], ((it >> 1) - 1) & 1, err))) break;
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->p_full[buf]);
+        if (lane == 0) mbar_arrive(&b->p_full[grp]);
       }
       if (!ok) break;
       slot += 2u * L::kCh * n;
-      // output row and partial slot of this segment; then the next one's queries, so that its first
-      // scores are computed during this epilogue
+      // output row and partial slot of this segment
       const int part = s.part;
-      const int h = s.kvh * a.group + rr0 + min(r, rows - 1) - tok * a.group;
-      uint16_t* out = a.o + static_cast<long long>(s.row0 + tok) * a.ldo + static_cast<long long>(h) * D;
-      if (n > 0 && !(ok = warp_wait(b, &b->s_full[(it - 1) % L::kBufs], ((it - 1) / L::kBufs) & 1, err))) break;
+      uint16_t* out = a.o + static_cast<long long>(s.row0 + tok0 + tok) * a.ldo + static_cast<long long>(s.kvh * a.group + head) * D;
       if (!(ok = fetch(++i))) break;
       float m = -INFINITY;
       if (n > 0) {
@@ -781,7 +827,6 @@ __global__ void __launch_bounds__(kThreads_, 1)
         if (!(ok = warp_wait(b, &b->o_done[(it - 1) & 1], ((it - 1) >> 1) & 1, err))) break;
         tc::fence_after_sync();
       }
-      queries_in();
       if (live) {
         if (n > 0) m = b->m[(it - 1) & 1][r];      // the last tile's
         if (ml != m) l *= ex2(ml - m);             // a group without a tile has l = 0 and ml = -inf
@@ -790,28 +835,30 @@ __global__ void __launch_bounds__(kThreads_, 1)
         l += b->l[grp ^ 1][r];
         if (!(ok = pair_sync(b, quarter, meets, err))) break;
         const float inv = l > 0.f ? 1.f / l : 0.f;   // a row that saw nothing takes exact zeros
+        // Columns in chunks of 64, every other one this group's. A lane has a row; after a transposition within 8
+        // lanes it has a 16-byte piece of 8 rows, so that a store writes 4 rows x 128 bytes (rows of 32 bytes
+        // took four times as long).
+        float* dst = a.part + (static_cast<long long>(part) * a.max_rows + r) * D;
 #pragma unroll 1
-        for (int c = grp * (D / 2); c < (grp + 1) * (D / 2); c += 32) {
-          float o[32];
+        for (int c = grp * 64; c < D; c += 128) {
+          float o[2][32];
           if (n > 0) {
-            tmem_ld32(tmem + lanes + c, o);
-            tmem_wait_ld(o);
+            tmem_ld32(tmem + lanes + c, o[0]);
+            tmem_ld32(tmem + lanes + c + 32, o[1]);
+            tmem_wait_ld(o[0]);
+            tmem_wait_ld(o[1]);
           } else {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0.f;
+            for (int k = 0; k < 64; ++k) o[k >> 5][k & 31] = 0.f;
           }
-          if (r < rows) {
-            if (part < 0) {
-              uint32_t u[16];
+          if (part < 0) {
+            uint32_t u[32];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) u[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
-              store_bf16x16(out + c, u);
-              store_bf16x16(out + c + 16, u + 8);
-            } else {
-              float* dst = a.part + (static_cast<long long>(part) * a.max_rows + r) * D + c;
-#pragma unroll
-              for (int k = 0; k < 32; k += 8) store32(dst + k, reinterpret_cast<const uint32_t*>(o) + k);
-            }
+            for (int k = 0; k < 32; ++k) u[k] = pack_bf16(o[k >> 4][2 * k & 31] * inv, o[k >> 4][(2 * k & 31) + 1] * inv);
+            store_rows(out + c, u, r, rows);
+          } else {
+            store_rows(dst + c, reinterpret_cast<uint32_t*>(o[0]), r, rows);
+            store_rows(dst + c + 32, reinterpret_cast<uint32_t*>(o[1]), r, rows);
           }
         }
         if (part >= 0 && grp == 0 && r < rows) a.ml[static_cast<long long>(part) * a.max_rows + r] = make_float2(m, l);
@@ -895,7 +942,7 @@ __global__ void __launch_bounds__(256) join_parts(const __grid_constant__ AttnAr
         for (int e = 0; e < E; ++e) o[e] += so[warp + k][lane * E + e] * f;
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int rr = tile * kM + r, tok = rr / a.group, h = kvh * a.group + rr - tok * a.group;
+      const int tr = r / a.group, tok = tile * a.tokens + tr, h = kvh * a.group + r - tr * a.group;
       uint32_t* out = reinterpret_cast<uint32_t*>(a.o + static_cast<long long>(row0 + tok) * a.ldo + static_cast<long long>(h) * D + lane * E);
 #pragma unroll
       for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
@@ -905,7 +952,7 @@ __global__ void __launch_bounds__(256) join_parts(const __grid_constant__ AttnAr
 }
 
 template <int D>
-cudaError_t launch_attn(const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, int grid, cudaStream_t s) {
+cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, int grid, cudaStream_t s) {
   static std::atomic<uint64_t> attr_set{0};   // per device
   cudaError_t e = once_per_device(attr_set, [] {
     return cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kSmem);
@@ -922,7 +969,7 @@ cudaError_t launch_attn(const CUtensorMap& tk, const CUtensorMap& tv, const Attn
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads_);
   cfg.dynamicSmemBytes = Lay<D>::kSmem;
-  e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D>, tk, tv, a);
+  e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D>, tq, tq1, tk, tv, a);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(2 * grid, std::min(kJoinY, a.max_rows));
   cfg.blockDim = dim3(256);
@@ -970,7 +1017,7 @@ int sm_count() {
 
 // ---------------------------------------------------------------- C ABI
 extern "C" size_t mk_paged_attention_scratch(const mk_paged_cache* c, int32_t rows, int32_t q_heads) {
-  if (mk::paged_cache_problem(c) || rows < 0 || q_heads < 1 || q_heads % c->kv_heads) return 0;
+  if (mk::paged_cache_problem(c) || rows < 0 || q_heads < 1 || q_heads % c->kv_heads || q_heads / c->kv_heads > mk::kM) return 0;
   return mk::scratch_of(mk::sm_count(), mk::max_rows_of(c, rows, q_heads), c->head_dim).total;
 }
 
@@ -983,7 +1030,7 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
   if (rows < 0 || n < 0 || n > 65536) return refuse("rows must not be negative, n must lie in 0 .. 65536");
   if (q_heads < 1 || q_heads % c->kv_heads) return refuse("q_heads must be a positive multiple of kv_heads");
   if (!(scale > -INFINITY && scale < INFINITY)) return refuse("scale must be finite");
-  if (static_cast<int64_t>(rows) * (q_heads / c->kv_heads) > (1 << 30)) return refuse("rows * group must be at most 2^30");
+  if (q_heads / c->kv_heads > mk::kM) return refuse("at most 128 query heads per kv head");
   if (rows == 0 || n == 0) return MK_OK;
   const int64_t dq = static_cast<int64_t>(q_heads) * c->head_dim;
   if (!d_q || !d_out || !d_seq_start || !d_scratch) return refuse("NULL pointer");
@@ -1004,16 +1051,23 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
     // masked score stays minus infinity
     const float c2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1e-30f);
     const mk::AttnArgs a{*c, layer, rows, q_heads, q_heads / c->kv_heads, box, static_cast<const uint16_t*>(d_q), ldq,
-                         static_cast<uint16_t*>(d_out), ldo, c2, scale < 0 ? 1 : 0,
+                         static_cast<uint16_t*>(d_out), ldo, mk::kM / (q_heads / c->kv_heads),
+                         std::min(mk::kM / (q_heads / c->kv_heads), (rows + n - 1) / n), c->head_dim == 256 ? 2 : c->head_dim == 128 ? 4 : 6, c2, scale < 0 ? 1 : 0,
                          mk::NewRows{d_seq_start, d_seqs, n}, reinterpret_cast<float*>(ws), reinterpret_cast<float2*>(ws + sc.ml),
                          reinterpret_cast<int*>(ws + sc.meta), max_rows};
-    CUtensorMap tk, tv;
+    CUtensorMap tq, tq1, tk, tv;
+    const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim), static_cast<uint64_t>(q_heads), static_cast<uint64_t>(rows)};
+    const uint64_t strides[2] = {2ull * c->head_dim, 2ull * ldq};
+    const uint32_t boxes[3] = {64, static_cast<uint32_t>(a.group), static_cast<uint32_t>(a.tokens)};
+    const uint32_t boxes1[3] = {64, static_cast<uint32_t>(a.group), static_cast<uint32_t>(a.few)};
+    if (!mk::tensor_map_bf16_nd(&tq, d_q, 3, dims, strides, boxes) || !mk::tensor_map_bf16_nd(&tq1, d_q, 3, dims, strides, boxes1))
+      return refuse("the queries' pitch cannot be described to the copy engine");
     if (!mk::page_map(&tk, *c, c->k, layer, box) || !mk::page_map(&tv, *c, c->v, layer, box))
       return refuse("the cache's strides cannot be described to the copy engine");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    e = c->head_dim == 256   ? mk::launch_attn<256>(tk, tv, a, grid, s)
-        : c->head_dim == 128 ? mk::launch_attn<128>(tk, tv, a, grid, s)
-                             : mk::launch_attn<64>(tk, tv, a, grid, s);
+    e = c->head_dim == 256   ? mk::launch_attn<256>(tq, tq1, tk, tv, a, grid, s)
+        : c->head_dim == 128 ? mk::launch_attn<128>(tq, tq1, tk, tv, a, grid, s)
+                             : mk::launch_attn<64>(tq, tq1, tk, tv, a, grid, s);
   }
   if (e == cudaSuccess) return MK_OK;
   mk_set_last_error(std::string("mk_paged_attention: ") + cudaGetErrorString(e));

@@ -430,7 +430,7 @@ int mk_qk_norm_rope(const mk_qk_rope* a, void* stream);
  * last page or in pages the table does not name, is never part of a result. A page id out of range sets
  * MK_DEVERR_BAD_PAGE and reads as zeros.
  * d_q: bf16 [rows][q_heads][head_dim], d_out: bf16 likewise, ldq / ldo elements from row to
- * row (multiples of 8); 16-byte aligned. n <= 65536. q_heads a multiple of the cache's kv_heads.
+ * row (multiples of 8); 16-byte aligned. n <= 65536. q_heads a multiple of the cache's kv_heads, at most 128 times them.
  * d_scratch: at least mk_paged_attention_scratch(...) bytes, 32-byte aligned; one buffer per
  * call that may run at the same time. */
 int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const void* d_q, int64_t ldq, int32_t rows, int32_t q_heads,

@@ -187,7 +187,8 @@ def run_attention(seed, lens, new, hq, hkv, d, ps, scale=None, poison=True, laye
 
 
 @pytest.mark.parametrize("hq,hkv,d,ps", [(8, 2, 256, 64), (24, 4, 256, 16), (4, 1, 64, 8), (16, 4, 128, 48), (3, 3, 64, 128), (7, 1, 128, 24),
-                                         (8, 1, 256, 256), (5, 1, 256, 32)])
+                                         (8, 1, 256, 256), (5, 1, 256, 32), (128, 1, 64, 16), (100, 1, 128, 32),
+                                         (130, 2, 64, 64)])
 def test_attention_ragged_lengths(hq, hkv, d, ps):
     lens = [1, 0, 64, 127, 128, 129, 300, 5, ps, 2 * ps + 1, 77]
     new = [1, 0, 1, 3, 128, 129, 44, 5, 1, 2 * ps, 0]

@@ -123,7 +123,7 @@ def test_attention_refuses(lib):
                                       v["scale"], v["out"], v["ldo"], v["scr"], v["size"], None)
 
     for kw in (dict(layer=2), dict(layer=-1), dict(q=None), dict(q=A + 8), dict(out=None), dict(out=A + 2), dict(ldq=1016),
-               dict(ldq=1028), dict(ldo=8), dict(rows=-1), dict(hq=0), dict(hq=7), dict(start=None), dict(n=-1), dict(n=65537),
+               dict(ldq=1028), dict(ldo=8), dict(rows=-1), dict(hq=0), dict(hq=7), dict(hq=258, ldq=1 << 16, ldo=1 << 16), dict(start=None), dict(n=-1), dict(n=65537),
                dict(scale=float("inf")), dict(scale=float("nan")), dict(scr=None), dict(scr=A + 4), dict(size=0)):
         assert call(**kw) == _abi.MK_ERR_ARG, kw
     assert call(rows=0) == _abi.MK_OK and call(n=0) == _abi.MK_OK
