@@ -81,13 +81,12 @@ struct AttnArgs {
   NewRows w;
   float* part;             // [2 * grid][max_rows][D]
   float2* ml;              // [2 * grid][max_rows] (m, l)
-  int* meta;               // [2 * grid][kMeta]
+  int4* lead;              // [2 * grid]: what each CTA leads, see below
   int max_rows;
 };
-// Partial results of one slot: first / last flags (kPart*), rows, first packed row, kv head, the
-// sequence's first row.
-constexpr int kMeta = 8;
-constexpr int kPartUsed = 1, kPartFirst = 2, kPartLast = 4;
+// The row tile whose first keys a CTA has and whose others it leaves to the next ones (its last segment, so one
+// at most): {slot of its partial results, contributors (0: none), rows, row tile}, {kv head, the sequence's first
+// row}. The other contributors are the next CTAs, each with its first slot.
 
 // One stretch of key tiles of one row tile.
 struct Segment {
@@ -368,7 +367,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int* err = a.c.err;
   if (smem_u32(smem) & 1023) {
-    if (threadIdx.x == 0) atomicOr(err, MK_DEVERR_PIPE_TIMEOUT);
+    if (threadIdx.x == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      a.lead[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
+      atomicOr(err, MK_DEVERR_PIPE_TIMEOUT);
+    }
     return;
   }
 
@@ -470,7 +473,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
       }
       __syncwarp();
     };
-    for (int k = lane; k < 2 * kMeta; k += 32) a.meta[blockIdx.x * 2 * kMeta + k] = 0;
+    if (lane == 0) a.lead[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     __syncwarp();
     long long u = u0;
     for (; u < u1 && ok && g < n_groups; ++g) {
@@ -514,13 +517,13 @@ __global__ void __launch_bounds__(kThreads_, 1)
         const bool whole = s.t0 == 0 && s.t1 == tiles;
         s.part = whole ? -1 : static_cast<int>(blockIdx.x) * 2 + (made ? 1 : 0);
         ++made;
-        if (!whole && lane == 0) {
-          int* m = a.meta + static_cast<long long>(s.part) * kMeta;
-          m[0] = kPartUsed | (s.t0 == 0 ? kPartFirst : 0) | (s.t1 == tiles ? kPartLast : 0);
-          m[1] = min(a.tokens, w.rows - s.tile * a.tokens) * a.group;
-          m[2] = s.tile;
-          m[3] = s.kvh;
-          m[4] = s.row0;
+        if (!whole && s.t0 == 0 && lane == 0) {
+          // the CTA whose run holds the row tile's last unit: the largest c with total c / ctas <= that unit
+          const long long end = u + (tiles - s.t1), ctas = min(static_cast<long long>(gridDim.x), total);
+          const int last = static_cast<int>((end * ctas + total - 1) / total) - 1;
+          a.lead[2 * blockIdx.x] = make_int4(s.part, last - static_cast<int>(blockIdx.x) + 1,
+                                             min(a.tokens, w.rows - s.tile * a.tokens) * a.group, s.tile);
+          a.lead[2 * blockIdx.x + 1] = make_int4(s.kvh, s.row0, 0, 0);
         }
         emit(s);
       }
@@ -876,35 +879,25 @@ __global__ void __launch_bounds__(kThreads_, 1)
 }
 
 // Joins the partial results of the row tiles whose keys were cut: with M the largest m of the
-// contributors, o = sum 2^(m - M) O / sum 2^(m - M) l. Contributors of a row tile are consecutive CTAs; the
-// slot of the first one leads. A block takes the rows y, y + gridDim.y, ... of one leading slot; its 8 warps share the
-// contributors of a row, or several rows where there are fewer, and are joined in a fixed order.
+// contributors, o = sum 2^(m - M) O / sum 2^(m - M) l. blockIdx.x is the leading CTA, blockIdx.y takes every
+// gridDim.y-th group of rows. Up to four contributors are read by one warp, all of a row's at once (a prompt's
+// row tile is cut once or twice, and there are many rows); more are shared by up to 8 warps of the block (a long
+// context's few rows have one contributor per CTA) and joined in a fixed order.
 constexpr int kJoinY = 16;
 template <int D>
-__global__ void __launch_bounds__(256) join_parts(const __grid_constant__ AttnArgs a, int slots) {
+__global__ void __launch_bounds__(256) join_parts(const __grid_constant__ AttnArgs a) {
   constexpr int E = D / 32;
   __shared__ float so[8][D];
   __shared__ float2 sm[8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lead = blockIdx.x;
-  const int* meta = a.meta + static_cast<long long>(lead) * kMeta;
-  if ((meta[0] & (kPartUsed | kPartFirst)) != (kPartUsed | kPartFirst)) return;
-  const int rows = meta[1], tile = meta[2], kvh = meta[3], row0 = meta[4];
-  // contributor k > 0 is slot 2 (lead / 2 + k); the last one is marked
-  const int cta = lead / 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int n = 0;
-  for (int base = 1;; base += 32) {
-    const int k = base + lane, slot = 2 * (cta + k);
-    const bool last = slot >= slots || (a.meta[static_cast<long long>(slot) * kMeta] & kPartLast);
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, last);
-    if (hit) {
-      n = min(base + __ffs(hit), slots / 2 - cta);
-      break;
-    }
-  }
+  const int cta = blockIdx.x;
+  const int4 lead = a.lead[2 * cta], where = a.lead[2 * cta + 1];
+  const int n = min(lead.y, static_cast<int>(gridDim.x) - cta), rows = lead.z;
+  if (n <= 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int per_row = 1;                                 // warps that share a row
-  while (per_row < 8 && per_row * 2 <= n) per_row *= 2;
+  while (per_row < 8 && per_row * 4 < n) per_row *= 2;
   const int at_once = 8 / per_row, sub = warp % per_row;
   for (int first = blockIdx.y * at_once; first < rows; first += gridDim.y * at_once) {
     const int r = first + warp / per_row;
@@ -912,42 +905,75 @@ __global__ void __launch_bounds__(256) join_parts(const __grid_constant__ AttnAr
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
     if (r < rows) {
-#pragma unroll 4
-      for (int k = sub; k < n; k += per_row) {
-        const long long at = static_cast<long long>(k ? 2 * (cta + k) : lead) * a.max_rows + r;
-        const float2 ml = a.ml[at];
-        const float* src = a.part + at * D + lane * E;
-        const float top = fmaxf(m, ml.x), f = top == -INFINITY ? 0.f : ex2(m - top), w = top == -INFINITY ? 0.f : ex2(ml.x - top);
-        l = l * f + ml.y * w;
+      for (int k0 = sub; k0 < n; k0 += 4 * per_row) {   // four contributors in flight
+        float2 ml[4];
+        float x[4][E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + src[e] * w;
+        for (int i = 0; i < 4; ++i) {
+          const int k = k0 + i * per_row;
+          ml[i] = make_float2(-INFINITY, 0.f);
+          if (k < n) {
+            const long long at = static_cast<long long>(k ? 2 * (cta + k) : lead.x) * a.max_rows + r;
+            ml[i] = a.ml[at];
+            const float* src = a.part + at * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const float2 v = *reinterpret_cast<const float2*>(src + e);
+              x[i][e] = v.x, x[i][e + 1] = v.y;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[i][e] = 0.f;
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, ml[i].x);
+        if (top == -INFINITY) continue;            // rows that see nothing so far
+        const float f = ex2(m - top);
+        l *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = ex2(ml[i].x - top);
+          l = fmaf(ml[i].y, w, l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(x[i][e], w, o[e]);
+        }
         m = top;
       }
     }
-    if (lane == 0) sm[warp] = make_float2(m, l);
+    if (per_row > 1) {                             // the same for the whole block
+      if (lane == 0) sm[warp] = make_float2(m, l);
 #pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-    __syncthreads();
-    if (sub == 0 && r < rows) {
-      float top = m;
-      for (int k = 1; k < per_row; ++k) top = fmaxf(top, sm[warp + k].x);
-      float f = top == -INFINITY ? 0.f : ex2(m - top);
-      l *= f;
+      for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
+      __syncthreads();
+      if (sub == 0) {
+        float top = m;
+        for (int k = 1; k < per_row; ++k) top = fmaxf(top, sm[warp + k].x);
+        if (top > -INFINITY) {
+          float f = ex2(m - top);
+          l *= f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= f;
-      for (int k = 1; k < per_row; ++k) {
-        f = top == -INFINITY ? 0.f : ex2(sm[warp + k].x - top);
-        l += sm[warp + k].y * f;
+          for (int e = 0; e < E; ++e) o[e] *= f;
+          for (int k = 1; k < per_row; ++k) {
+            f = ex2(sm[warp + k].x - top);
+            l += sm[warp + k].y * f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += so[warp + k][lane * E + e] * f;
+            for (int e = 0; e < E; ++e) o[e] += so[warp + k][lane * E + e] * f;
+          }
+        }
       }
+      __syncthreads();
+    }
+    if (sub == 0 && r < rows) {
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int tr = r / a.group, tok = tile * a.tokens + tr, h = kvh * a.group + r - tr * a.group;
-      uint32_t* out = reinterpret_cast<uint32_t*>(a.o + static_cast<long long>(row0 + tok) * a.ldo + static_cast<long long>(h) * D + lane * E);
+      const int tr = r / a.group, tok = lead.w * a.tokens + tr, h = where.x * a.group + r - tr * a.group;
+      uint32_t* out = reinterpret_cast<uint32_t*>(a.o + static_cast<long long>(where.y + tok) * a.ldo + static_cast<long long>(h) * D + lane * E);
 #pragma unroll
       for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
     }
-    __syncthreads();
   }
 }
 
@@ -971,10 +997,10 @@ cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tq1, const CUt
   cfg.dynamicSmemBytes = Lay<D>::kSmem;
   e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D>, tq, tq1, tk, tv, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(2 * grid, std::min(kJoinY, a.max_rows));
+  cfg.gridDim = dim3(grid, std::min(kJoinY, a.max_rows));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_parts<D>, a, 2 * grid);
+  return cudaLaunchKernelEx(&cfg, join_parts<D>, a);
 }
 
 // Key or value pages of a layer as a 4-D tensor: entries, slots, kv heads, pages; a box is 64 entries of `box` slots.
@@ -992,15 +1018,15 @@ int refuse(const std::string& why) {
 }
 
 struct Scratch {
-  size_t part, ml, meta, total;
+  size_t part, ml, lead, total;
 };
 Scratch scratch_of(int grid, int max_rows, int d) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   Scratch s{};
   const size_t rows = 2ull * grid * max_rows;
   s.ml = up(rows * d * sizeof(float));
-  s.meta = s.ml + up(rows * sizeof(float2));
-  s.total = s.meta + up(2ull * grid * kMeta * sizeof(int));
+  s.lead = s.ml + up(rows * sizeof(float2));
+  s.total = s.lead + up(2ull * grid * sizeof(int4));
   return s;
 }
 int max_rows_of(const mk_paged_cache* c, int rows, int q_heads) {
@@ -1054,7 +1080,7 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
                          static_cast<uint16_t*>(d_out), ldo, mk::kM / (q_heads / c->kv_heads),
                          std::min(mk::kM / (q_heads / c->kv_heads), (rows + n - 1) / n), c->head_dim == 256 ? 2 : c->head_dim == 128 ? 4 : 6, c2, scale < 0 ? 1 : 0,
                          mk::NewRows{d_seq_start, d_seqs, n}, reinterpret_cast<float*>(ws), reinterpret_cast<float2*>(ws + sc.ml),
-                         reinterpret_cast<int*>(ws + sc.meta), max_rows};
+                         reinterpret_cast<int4*>(ws + sc.lead), max_rows};
     CUtensorMap tq, tq1, tk, tv;
     const uint64_t dims[3] = {static_cast<uint64_t>(c->head_dim), static_cast<uint64_t>(q_heads), static_cast<uint64_t>(rows)};
     const uint64_t strides[2] = {2ull * c->head_dim, 2ull * ldq};
