@@ -54,12 +54,12 @@ struct Lay {
   static constexpr int kSlots = D == 256 ? 5 : D == 128 ? 6 : 8;
   static constexpr int kOffBars = kQ + kSlots * kSlot;
   static constexpr int kSmem = kOffBars + kBarBytes;
-  // TMEM columns: O [0, D), score buffers of 128 columns, two P buffers of 64. A softmax group holds its
-  // tile's scores in registers, so the next scores overwrite them as soon as they are loaded, and the chain
-  // from one tile of a group to its next is the softmax alone. 256 columns of O leave room
-  // for one score buffer, smaller ones for two, and the scores run that many tiles ahead of the products.
-  static constexpr int kBufs = D == 256 ? 1 : 2, kAhead = kBufs;
-  static constexpr uint32_t kColS = D, kColP = D + kBufs * 128;
+  // TMEM columns: O [0, D), then the score buffers of 128, whose first 64 columns take P. With three of
+  // them (head dims up to 128) the scores run two tiles ahead of the products, so a softmax group finds
+  // its next tile ready; 256 columns of O leave room for two. (P in columns of its own, so that scores could follow as
+  // soon as the last ones are in registers, was slower: its writers wait for the product two tiles before.)
+  static constexpr uint32_t kColS = D;
+  static constexpr int kBufs = D == 256 ? 2 : 3, kAhead = kBufs - 1;
   // Places of the n key and value tiles of a segment in the ring: the scores of kAhead + 1 tiles, the
   // first product, and so on in turn, the last kAhead products at the end.
   __device__ static int k_place(int j, int) { return j <= kAhead ? j : 2 * j - kAhead; }
@@ -102,7 +102,7 @@ struct Segment {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], s_full[2], s_free[2], p_full[2], o_done[2], q_full, q_free, pair[4], m_full[2][4], seg_full[kSegs], seg_empty[kSegs];
+  uint64_t full[8], empty[8], s_full[3], p_full[3], o_done[2], q_full, q_free, pair[4], m_full[2][4], seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem;
   int abort;
   Segment seg[kSegs];
@@ -381,12 +381,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
       mbar_init(&b->full[i], 1);
       mbar_init(&b->empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {              // by tile parity: each is one softmax group's
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&b->s_full[i], 1);
-      mbar_init(&b->s_free[i], kSoftWarps / 2);
       mbar_init(&b->p_full[i], kSoftWarps / 2);
-      mbar_init(&b->o_done[i], 1);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&b->o_done[i], 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(&b->pair[i], 2);
       mbar_init(&b->m_full[0][i], 1);
@@ -621,14 +620,9 @@ __global__ void __launch_bounds__(kThreads_, 1)
       commit(&b->empty[k], issue);
       if (++k == L::kSlots) k = 0, phase ^= 1;
     };
-    uint32_t ahead = 0;                            // tiles whose scores were issued
-    auto scores = [&] {
-      const uint32_t d = tmem + L::kColS + ahead % L::kBufs * kN;
-      if (ahead >= L::kBufs) {                     // the buffer's last scores are in registers
-        const uint32_t was = ahead - L::kBufs;
-        if (!(ok = ok && warp_wait(b, &b->s_free[was & 1], (was >> 1) & 1, err))) return;
-        tc::fence_after_sync();
-      }
+    uint32_t sbuf = 0, pbuf = 0, pphase = 0;       // score buffer of the next scores; of the next product, and its phase
+    auto scores = [&] {                            // the buffer's P was consumed by a product issued before
+      const uint32_t d = tmem + L::kColS + sbuf * kN;
 #pragma unroll
       for (int c = 0; c < L::kCh; ++c) {
         if (!take()) return;
@@ -641,8 +635,8 @@ __global__ void __launch_bounds__(kThreads_, 1)
                    (c | p | kk) ? 1u : 0u, issue);
         pass();
       }
-      commit(&b->s_full[ahead & 1], issue);
-      ++ahead;
+      commit(&b->s_full[sbuf], issue);
+      sbuf = sbuf == L::kBufs - 1 ? 0 : sbuf + 1;
     };
     for (int i = 0; ok; ++i) {
       if (!warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) break;
@@ -660,8 +654,9 @@ __global__ void __launch_bounds__(kThreads_, 1)
           scores();
           if (t + L::kAhead == n - 1) commit(&b->q_free, issue);
         }
-        if (!ok || !(ok = warp_wait(b, &b->p_full[it & 1], (it >> 1) & 1, err))) break;
-        const uint32_t pa = tmem + L::kColP + (it & 1) * (kN / 2), more = t > 0;
+        if (!ok || !(ok = warp_wait(b, &b->p_full[pbuf], pphase, err))) break;
+        const uint32_t pa = tmem + L::kColS + pbuf * kN, more = t > 0;
+        if (++pbuf == L::kBufs) pbuf = 0, pphase ^= 1;
 #pragma unroll
         for (int c = 0; c < L::kCh; ++c) {
           if (!take()) break;
@@ -705,7 +700,10 @@ __global__ void __launch_bounds__(kThreads_, 1)
       for (int j = 0; j < n; ++j, ++it) {
         if ((it & 1) != static_cast<uint32_t>(grp)) continue;
         const int t = s.t0 + j;
-        if (!(ok = warp_wait(b, &b->s_full[grp], (it >> 1) & 1, err))) break;
+        const uint32_t buf = it % L::kBufs, sb = tmem + lanes + L::kColS + buf * kN;
+        // (of the tiles that had this buffer before, the last one's scores are complete: they were issued before
+        // those of this group's last tile, so no phase is skipped)
+        if (!(ok = warp_wait(b, &b->s_full[buf], (it / L::kBufs) & 1, err))) break;
         if (live) {
           tc::fence_after_sync();
           const int key0 = t * kN;
@@ -713,12 +711,9 @@ __global__ void __launch_bounds__(kThreads_, 1)
           // the row's 128 scores stay in registers: four loads in flight, and one pass for the maximum
           float x[kN];
 #pragma unroll
-          for (int c = 0; c < kN; c += 32) tmem_ld32(tmem + lanes + L::kColS + it % L::kBufs * kN + c, x + c);
+          for (int c = 0; c < kN; c += 32) tmem_ld32(sb + c, x + c);
 #pragma unroll
           for (int c = 0; c < kN; c += 32) tmem_wait_ld(x + c);
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&b->s_free[grp]);
           if (a.negative) {
 #pragma unroll
             for (int c = 0; c < kN; ++c) x[c] = -x[c];
@@ -763,11 +758,6 @@ __global__ void __launch_bounds__(kThreads_, 1)
             }
             tmem_wait_st();
           }
-          // P's columns are free once this group's product before is done (it was its own wait's phase)
-          if (it >= 2) {
-            if (!(ok = warp_wait(b, &b->o_done[grp], ((it >> 1) - 1) & 1, err))) break;
-            tc::fence_after_sync();
-          }
           if (ml != m) l *= ex2(ml - m);           // m may have been raised at the other group's tile
           ml = m;
           const float sub = m == -INFINITY ? 0.f : -m;
@@ -786,16 +776,12 @@ __global__ void __launch_bounds__(kThreads_, 1)
               p[k] = pack_bf16(p0, p1);
               p[k + 1] = pack_bf16(p2, p3);
             }
-            tmem_st16(tmem + lanes + L::kColP + grp * (kN / 2) + c / 2, p);
+            tmem_st16(sb + c / 2, p);              // over the scores, which have all been loaded
           }
           tmem_wait_st();
           l += f2_sum(add2(sum0, sum1));
-        } else {
-          if (lane == 0) {                         // nothing to load or to pass on, but the phases count tiles
-            mbar_arrive(&b->s_free[grp]);
-            mbar_arrive(&b->m_full[grp][quarter]);
-          }
-          if (it >= 2 && !(ok = warp_wait(b, &b->o_done[grp], ((it >> 1) - 1) & 1, err))) break;
+        } else if (lane == 0) {
+          mbar_arrive(&b->m_full[grp][quarter]);   // nothing to pass on, but the phases count tiles
         }
         if ((t + 1) * kN > s.len) {
           // positions from len on: whatever lies there must not meet a weight of zero as NaN
@@ -813,9 +799,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
           if (!ok) break;
           tc::fence_proxy_async_smem();
         }
+        // this group's product before is done by now, but a parity wait must not skip a phase
+        if (it >= 2 && !(ok = warp_wait(b, &b->o_done[grp], ((it >> 1) - 1) & 1, err))) break;
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b->p_full[grp]);
+        if (lane == 0) mbar_arrive(&b->p_full[buf]);
       }
       if (!ok) break;
       slot += 2u * L::kCh * n;
