@@ -207,33 +207,15 @@ __device__ __forceinline__ void tma_box3(void* dst, const CUtensorMap* map, int 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
-// Each lane has 128 bytes of its row r at p (32 registers, 8 pieces of 16 bytes); rows from `rows` on are not
-// written. The pieces are transposed within groups of 8 lanes (three exchanges of halves), the addresses with them.
-__device__ __forceinline__ void store_rows(void* p, uint32_t* u, int r, int rows) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int s = 4; s >= 1; s /= 2) {
-    const bool up = lane & s;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (k & s) continue;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t &lo = u[4 * k + c], &hi = u[4 * (k + s) + c];
-        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, s);
-        if (up)
-          lo = got;
-        else
-          hi = got;
-      }
-    }
-  }
-  const long long at = reinterpret_cast<long long>(p);
-  const int first = r - (lane & 7);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const long long to = __shfl_sync(0xFFFFFFFFu, at, (lane & ~7) + k) + (lane & 7) * 16;
-    if (first + k < rows) *reinterpret_cast<uint4*>(to) = make_uint4(u[4 * k], u[4 * k + 1], u[4 * k + 2], u[4 * k + 3]);
+// 32 bytes to a 32-byte aligned address in one store (a whole sector), or to a 16-byte aligned one in two.
+__device__ __forceinline__ void store32(void* p, const uint32_t* u) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]),
+                 "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(u[4], u[5], u[6], u[7]);
   }
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -826,30 +808,30 @@ __global__ void __launch_bounds__(kThreads_, 1)
         l += b->l[grp ^ 1][r];
         if (!(ok = pair_sync(b, quarter, meets, err))) break;
         const float inv = l > 0.f ? 1.f / l : 0.f;   // a row that saw nothing takes exact zeros
-        // Columns in chunks of 64, every other one this group's. A lane has a row; after a transposition within 8
-        // lanes it has a 16-byte piece of 8 rows, so that a store writes 4 rows x 128 bytes (rows of 32 bytes
-        // took four times as long).
+        // half the columns each, every lane its row in whole sectors (transposing within 8 lanes, for 128-byte stores,
+        // was no faster)
         float* dst = a.part + (static_cast<long long>(part) * a.max_rows + r) * D;
 #pragma unroll 1
-        for (int c = grp * 64; c < D; c += 128) {
-          float o[2][32];
+        for (int c = grp * (D / 2); c < (grp + 1) * (D / 2); c += 32) {
+          float o[32];
           if (n > 0) {
-            tmem_ld32(tmem + lanes + c, o[0]);
-            tmem_ld32(tmem + lanes + c + 32, o[1]);
-            tmem_wait_ld(o[0]);
-            tmem_wait_ld(o[1]);
+            tmem_ld32(tmem + lanes + c, o);
+            tmem_wait_ld(o);
           } else {
 #pragma unroll
-            for (int k = 0; k < 64; ++k) o[k >> 5][k & 31] = 0.f;
+            for (int k = 0; k < 32; ++k) o[k] = 0.f;
           }
-          if (part < 0) {
-            uint32_t u[32];
+          if (r < rows) {
+            if (part < 0) {
+              uint32_t u[16];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) u[k] = pack_bf16(o[k >> 4][2 * k & 31] * inv, o[k >> 4][(2 * k & 31) + 1] * inv);
-            store_rows(out + c, u, r, rows);
-          } else {
-            store_rows(dst + c, reinterpret_cast<uint32_t*>(o[0]), r, rows);
-            store_rows(dst + c + 32, reinterpret_cast<uint32_t*>(o[1]), r, rows);
+              for (int k = 0; k < 16; ++k) u[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+              store32(out + c, u);
+              store32(out + c + 16, u + 8);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; k += 8) store32(dst + c + k, reinterpret_cast<const uint32_t*>(o) + k);
+            }
           }
         }
         if (part >= 0 && grp == 0 && r < rows) a.ml[static_cast<long long>(part) * a.max_rows + r] = make_float2(m, l);

@@ -404,28 +404,52 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_fork(mk_paged_cache c, c
 
 // mk_pages_compact, counts and copies: pages in use, then the r-th used page with an id past
 // them paired with the r-th free id below (there are equally many). list[p] is the new id of
-// a moved page p; the table follows in remap_table.
+// a moved page p; the table follows in the copy kernel. Four counts a thread and step.
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_compact(mk_paged_cache c) {
   __shared__ int red[32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Work w = work_of(c);
   const int tid = threadIdx.x;
+  const bool wide = (reinterpret_cast<uintptr_t>(c.ref) & 15) == 0;
+  auto four = [&](long long p) {               // counts of pages p .. p + 3, 0 past the last one
+    if (wide && p + 4 <= c.n_pages) return *reinterpret_cast<const int4*>(c.ref + p);
+    int4 v = make_int4(0, 0, 0, 0);
+    if (p < c.n_pages) v.x = c.ref[p];
+    if (p + 1 < c.n_pages) v.y = c.ref[p + 1];
+    if (p + 2 < c.n_pages) v.z = c.ref[p + 2];
+    if (p + 3 < c.n_pages) v.w = c.ref[p + 3];
+    return v;
+  };
   int used = 0;
-  for (int p = tid; p < c.n_pages; p += kPlanThreads) used += c.ref[p] > 0;
-  int total;
-  block_scan(used, &total, red);
-  const int live = total;
+#pragma unroll 4
+  for (long long p = 4ll * tid; p < c.n_pages; p += 4 * kPlanThreads) {
+    const int4 v = four(p);
+    used += (v.x > 0) + (v.y > 0) + (v.z > 0) + (v.w > 0);
+  }
+  int live;
+  block_scan(used, &live, red);
   int holes = 0, movers = 0;
-  for (long long base = 0; base < c.n_pages; base += kPlanThreads) {
-    const long long p = base + tid;
-    const bool in = p < c.n_pages;
-    const int r = in ? c.ref[p] : 0;
-    const bool hole = in && p < live && r <= 0, mover = in && p >= live && r > 0;
-    // both counts in one scan: holes in the low half, movers in the high half
-    const int s = block_scan(static_cast<int>(hole) | static_cast<int>(mover) << 16, &total, red);
-    if (hole) w.dst[holes + (s & 0xFFFF)] = static_cast<int>(p);
-    if (mover) {
-      w.src[movers + (s >> 16)] = static_cast<int>(p);
-      w.rows[movers + (s >> 16)] = c.page_size;
+  for (long long base = 0; base < c.n_pages; base += 4 * kPlanThreads) {
+    const long long p = base + 4 * tid;
+    const int4 v = four(p);
+    const int r[4] = {v.x, v.y, v.z, v.w};
+    unsigned hole = 0, mover = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (p + k >= c.n_pages) continue;
+      hole |= (p + k < live && r[k] <= 0) << k;
+      mover |= (p + k >= live && r[k] > 0) << k;
+    }
+    int total;   // both counts in one scan: holes in the low half, movers in the high half
+    const int s = block_scan(static_cast<int>(__popc(hole) | __popc(mover) << 16), &total, red);
+    int h = holes + (s & 0xFFFF), m = movers + (s >> 16);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (hole >> k & 1) w.dst[h++] = static_cast<int>(p) + k;
+      if (mover >> k & 1) {
+        w.src[m] = static_cast<int>(p) + k;
+        w.rows[m++] = c.page_size;
+      }
     }
     holes += total & 0xFFFF;
     movers += total >> 16;
@@ -443,16 +467,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_compact(mk_paged_cache c
   }
 }
 
-__global__ void remap_table(mk_paged_cache c) {
+// The table entries of moved pages, by the whole grid of the copy kernel.
+__device__ void remap_table(const mk_paged_cache& c) {
   const Work w = work_of(c);
   const int live = w.count[1];
-  if (w.count[0] == 0) return;
-  const long long total = static_cast<long long>(c.n_seqs) * c.max_pages;
-  for (long long i = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const int s = static_cast<int>(i / c.max_pages), j = static_cast<int>(i % c.max_pages);
-    const int len = c.len[s], p = c.table[i];
-    if (static_cast<long long>(j) * c.page_size >= len || p < live || p >= c.n_pages) continue;
+  const unsigned total = static_cast<unsigned>(c.n_seqs) * c.max_pages;   // below 2^31 (checked by the host)
+  for (unsigned i = blockIdx.x * blockDim.x + threadIdx.x; i < total; i += gridDim.x * blockDim.x) {
+    const int s = i / c.max_pages, j = i - s * c.max_pages, p = c.table[i];
+    if (static_cast<long long>(j) * c.page_size >= c.len[s] || p < live || p >= c.n_pages) continue;
     // a page that is named but not counted in ref stays where it is
     const int to = w.list[p];
     if (to >= 0 && to < live) c.table[i] = to;
@@ -467,6 +489,7 @@ struct CopyArgs {
   const int *src, *dst, *rows;   // rows null: whole pages
   const int* count;              // null: n
   int n;
+  int remap;                     // compaction: the table follows the pages
   int* err;
 };
 constexpr int kCopyThreads = 256, kCopyPer = 8;
@@ -476,6 +499,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant
   const mk_paged_cache& f = a.from;
   const mk_paged_cache& t = a.to;
   const int count = a.count ? *a.count : a.n;
+  if (a.remap && count > 0) remap_table(f);
   const int dv = f.head_dim / 8, sh = __ffs(dv) - 1;   // vectors of a row (a power of two)
   const unsigned per_max = static_cast<unsigned>(f.n_layers) * 2u * f.kv_heads;   // (layer, K or V, head) triples
   const unsigned page_tasks = (per_max * f.page_size * dv + kCopyThreads * kCopyPer - 1) / (kCopyThreads * kCopyPer);
@@ -566,9 +590,9 @@ cudaError_t launch_plan(PlanKernel kernel, const mk_paged_cache& c, const int* a
   return cudaGetLastError();
 }
 
-cudaError_t copy_planned(const mk_paged_cache& c, long long pairs, cudaStream_t s) {
+cudaError_t copy_planned(const mk_paged_cache& c, long long pairs, int remap, cudaStream_t s) {
   const Work w = work_of(c);
-  return launch_copy(CopyArgs{c, c, w.src, w.dst, w.rows, w.count, 0, c.err}, pairs, s);
+  return launch_copy(CopyArgs{c, c, w.src, w.dst, w.rows, w.count, 0, remap, c.err}, pairs, s);
 }
 
 }  // namespace
@@ -589,7 +613,7 @@ extern "C" int mk_pages_resize(const mk_paged_cache* c, const int32_t* d_seqs, c
   if (!d_seqs) return mk::refuse(who, "NULL sequence ids");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = mk::launch_plan(mk::plan_resize, *c, d_seqs, d_lens, n, s);
-  if (e == cudaSuccess && d_lens) e = mk::copy_planned(*c, n, s);   // freeing replaces no page
+  if (e == cudaSuccess && d_lens) e = mk::copy_planned(*c, n, 0, s);   // freeing replaces no page
   return mk::done(who, e);
 }
 
@@ -602,7 +626,7 @@ extern "C" int mk_pages_fork(const mk_paged_cache* c, const int32_t* d_src, cons
   if (!d_src || !d_dst) return mk::refuse(who, "NULL sequence ids");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = mk::launch_plan(mk::plan_fork, *c, d_src, d_dst, n, s);
-  if (e == cudaSuccess) e = mk::copy_planned(*c, n, s);
+  if (e == cudaSuccess) e = mk::copy_planned(*c, n, 0, s);
   return mk::done(who, e);
 }
 
@@ -613,12 +637,7 @@ extern "C" int mk_pages_compact(const mk_paged_cache* c, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   mk::plan_compact<<<1, mk::kPlanThreads, 0, s>>>(*c);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) {
-    const long long entries = static_cast<long long>(c->n_seqs) * c->max_pages;
-    mk::remap_table<<<static_cast<int>(std::min<long long>((entries + 255) / 256, 148 * 8)), 256, 0, s>>>(*c);
-    e = cudaGetLastError();
-  }
-  if (e == cudaSuccess) e = mk::copy_planned(*c, c->n_pages / 2 + 1, s);
+  if (e == cudaSuccess) e = mk::copy_planned(*c, c->n_pages / 2 + 1, 1, s);
   return mk::done(who, e);
 }
 
@@ -634,6 +653,6 @@ extern "C" int mk_pages_copy(const mk_paged_cache* from, const mk_paged_cache* t
   if (n < 0) return mk::refuse(who, "negative count");
   if (n == 0) return MK_OK;
   if (!d_src || !d_dst) return mk::refuse(who, "NULL page ids");
-  return mk::done(who, mk::launch_copy(mk::CopyArgs{*from, *to, d_src, d_dst, nullptr, nullptr, n, to->err}, n,
+  return mk::done(who, mk::launch_copy(mk::CopyArgs{*from, *to, d_src, d_dst, nullptr, nullptr, n, 0, to->err}, n,
                                        static_cast<cudaStream_t>(stream)));
 }
