@@ -7,7 +7,7 @@
 // per SM), so a single long sequence spreads over the whole GPU and ragged ones balance; a row
 // tile whose key range is cut leaves partial results (O, m, l), which a second kernel joins.
 //
-// Per key tile, with the scores in log2 units (c = scale log2 e):
+// Per key tile, with the scores in log2 units (c = |scale| log2 e, Q negated where the scale is):
 //   S = Q K^T                         tcgen05, M = 128, N = 128, K = D, into TMEM
 //   m = max(m, rowmax(c S));  P = 2^(c S - m), masked above the diagonal;  l += rowsum(P)
 //   O = O + P V                       tcgen05, P (bf16) read from TMEM
@@ -190,7 +190,7 @@ __device__ __forceinline__ void commit(uint64_t* bar, uint32_t issue) {
       "r"(issue)
       : "memory");
 }
-constexpr uint32_t kBMajorMN = 1u << 16;   // instruction descriptor: B is MN-major
+constexpr uint32_t kBMajorMN = 1u << 16, kNegateA = 1u << 13;   // instruction descriptor: B is MN-major; A negated
 
 // One box of a 4-D tensor map.
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
@@ -587,8 +587,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
     }
     __syncwarp();
   } else if (warp == 9) {
-    // ---- MMA issuer (all lanes, one issues). Values are read as they lie in a slot: MN-major.
-    constexpr uint32_t id_s = tc::idesc_bf16_f32(kM, kN), id_o = tc::idesc_bf16_f32(kM, L::kCW) | kBMajorMN;
+    // ---- MMA issuer (all lanes, one issues). Values are read as they lie in a slot: MN-major. The loops over
+    // slots and panels stay loops: unrolled, this role's code made every role of its scheduler slower
+    // (4096-token prompt of 256-wide heads 92 against 80 us).
+    constexpr uint32_t id_o = tc::idesc_bf16_f32(kM, L::kCW) | kBMajorMN;
+    const uint32_t id_s = tc::idesc_bf16_f32(kM, kN) | (a.negative ? kNegateA : 0u);   // the sign of the scale
     const uint32_t issue = elect_lane();
     const uint32_t q_lo = (smem_u32(smem) >> 4) | kLoK, ring_lo = smem_u32(ring) >> 4;
     uint32_t k = 0, phase = 0, it = 0, nq = 0;     // next ring slot and its phase
@@ -605,11 +608,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
     uint32_t sbuf = 0, pbuf = 0, pphase = 0;       // score buffer of the next scores; of the next product, and its phase
     auto scores = [&] {                            // the buffer's P was consumed by a product issued before
       const uint32_t d = tmem + L::kColS + sbuf * kN;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < L::kCh; ++c) {
         if (!take()) return;
         const uint32_t b_lo = (ring_lo + k * (L::kSlot >> 4)) | kLoK;
-#pragma unroll
+#pragma unroll 1
         for (int p = 0; p < L::kCW / 64; ++p)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -629,17 +632,16 @@ __global__ void __launch_bounds__(kThreads_, 1)
       if (len == 0) continue;
       if (!(ok = warp_wait(b, &b->q_full, nq++ & 1, err))) break;
       tc::fence_after_sync();
-      for (int t = 0; t < L::kAhead && t < n; ++t) scores();
-      if (n <= L::kAhead) commit(&b->q_free, issue);
-      for (int t = 0; t < n && ok; ++t, ++it) {
+      for (int t = -L::kAhead; t < n && ok; ++t) {
         if (t + L::kAhead < n) {
           scores();
           if (t + L::kAhead == n - 1) commit(&b->q_free, issue);
         }
+        if (t < 0) continue;
         if (!ok || !(ok = warp_wait(b, &b->p_full[pbuf], pphase, err))) break;
         const uint32_t pa = tmem + L::kColS + pbuf * kN, more = t > 0;
         if (++pbuf == L::kBufs) pbuf = 0, pphase ^= 1;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < L::kCh; ++c) {
           if (!take()) break;
           const uint32_t b_lo = (ring_lo + k * (L::kSlot >> 4)) | kLoMN;
@@ -649,6 +651,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
           pass();
         }
         if (ok) commit(&b->o_done[it & 1], issue);
+        ++it;
       }
     }
     __syncwarp();
@@ -696,10 +699,6 @@ __global__ void __launch_bounds__(kThreads_, 1)
           for (int c = 0; c < kN; c += 32) tmem_ld32(sb + c, x + c);
 #pragma unroll
           for (int c = 0; c < kN; c += 32) tmem_wait_ld(x + c);
-          if (a.negative) {
-#pragma unroll
-            for (int c = 0; c < kN; ++c) x[c] = -x[c];
-          }
           if (masked) {
 #pragma unroll
             for (int c = 0; c < kN; ++c) x[c] = key0 + c <= pos ? x[c] : -INFINITY;
@@ -849,101 +848,114 @@ __global__ void __launch_bounds__(kThreads_, 1)
 }
 
 // Joins the partial results of the row tiles whose keys were cut: with M the largest m of the
-// contributors, o = sum 2^(m - M) O / sum 2^(m - M) l. blockIdx.x is the leading CTA, blockIdx.y takes every
-// gridDim.y-th group of rows. Up to four contributors are read by one warp, all of a row's at once (a prompt's
-// row tile is cut once or twice, and there are many rows); more are shared by up to 8 warps of the block (a long
-// context's few rows have one contributor per CTA) and joined in a fixed order.
-constexpr int kJoinY = 16;
+// contributors, o = sum 2^(m - M) O / sum 2^(m - M) l. blockIdx.x is the leading CTA; a task is (up to) 128 columns of
+// a row. Up to four contributors (a prompt's row tile is cut once or twice, and there are many rows) are
+// read at once by one warp, for two tasks at a time; more (a long context's few rows have one contributor
+// per CTA) are shared by the 8 warps of a block and joined in a fixed order.
+constexpr int kJoinY = 8;
+template <int D>
+struct Joined {
+  static constexpr int kCols = D < 128 ? D : 128, E = kCols / 32, kParts = D / kCols;
+  float m = -INFINITY, l = 0.f, o[E] = {};
+  int r, col;
+  __device__ Joined(int task, int lane) : r(task / kParts), col(task % kParts * kCols + lane * E) {}
+  // contributors k0, k0 + step, .. (four of them, below n)
+  __device__ __forceinline__ void take(const AttnArgs& a, int cta, int lead, int k0, int step, int n) {
+    float2 ml[4];
+    float x[4][E];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = k0 + i * step;
+      ml[i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[i][e] = 0.f;
+      if (k < n) {
+        const long long at = static_cast<long long>(k ? 2 * (cta + k) : lead) * a.max_rows + r;
+        ml[i] = a.ml[at];
+        const float* src = a.part + at * D + col;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          x[i][0] = v.x, x[i][1] = v.y;
+        }
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, ml[i].x);
+    const float base = top == -INFINITY ? 0.f : top;   // a row that sees nothing so far
+    const float f = ex2(m - base);
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float w = ex2(ml[i].x - base);
+      l = fmaf(ml[i].y, w, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(x[i][e], w, o[e]);
+    }
+    m = top;
+  }
+  __device__ __forceinline__ void store(const AttnArgs& a, int tile, int kvh, int row0) const {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int tr = r / a.group, tok = tile * a.tokens + tr, h = kvh * a.group + r - tr * a.group;
+    uint32_t* out = reinterpret_cast<uint32_t*>(a.o + static_cast<long long>(row0 + tok) * a.ldo + static_cast<long long>(h) * D + col);
+    if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    else
+      *out = pack_bf16(o[0] * inv, o[1] * inv);
+  }
+};
 template <int D>
 __global__ void __launch_bounds__(256) join_parts(const __grid_constant__ AttnArgs a) {
-  constexpr int E = D / 32;
-  __shared__ float so[8][D];
+  using J = Joined<D>;
+  constexpr int E = J::E;
+  __shared__ float so[8][J::kCols];
   __shared__ float2 sm[8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int cta = blockIdx.x;
   const int4 lead = a.lead[2 * cta], where = a.lead[2 * cta + 1];
-  const int n = min(lead.y, static_cast<int>(gridDim.x) - cta), rows = lead.z;
+  const int n = min(lead.y, static_cast<int>(gridDim.x) - cta), tasks = lead.z * J::kParts;
   if (n <= 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int per_row = 1;                                 // warps that share a row
-  while (per_row < 8 && per_row * 4 < n) per_row *= 2;
-  const int at_once = 8 / per_row, sub = warp % per_row;
-  for (int first = blockIdx.y * at_once; first < rows; first += gridDim.y * at_once) {
-    const int r = first + warp / per_row;
-    float m = -INFINITY, l = 0.f, o[E];
+  if (n <= 4) {
+    const int stride = gridDim.y * 8;
+    for (int t = blockIdx.y * 8 + warp; t < tasks; t += 2 * stride) {
+      J x(t, lane), y(min(t + stride, tasks - 1), lane);
+      x.take(a, cta, lead.x, 0, 1, n);
+      y.take(a, cta, lead.x, 0, 1, n);
+      x.store(a, lead.w, where.x, where.y);
+      if (t + stride < tasks) y.store(a, lead.w, where.x, where.y);
+    }
+    return;
+  }
+  for (int t = blockIdx.y; t < tasks; t += gridDim.y) {
+    J x(t, lane);
+    for (int k0 = warp; k0 < n; k0 += 32) x.take(a, cta, lead.x, k0, 8, n);
+    if (lane == 0) sm[warp] = make_float2(x.m, x.l);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    if (r < rows) {
-      for (int k0 = sub; k0 < n; k0 += 4 * per_row) {   // four contributors in flight
-        float2 ml[4];
-        float x[4][E];
+    for (int e = 0; e < E; ++e) so[warp][lane * E + e] = x.o[e];
+    __syncthreads();
+    if (warp == 0) {
+      float top = -INFINITY;
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, sm[k].x);
+      const float base = top == -INFINITY ? 0.f : top;
+      x.l = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = k0 + i * per_row;
-          ml[i] = make_float2(-INFINITY, 0.f);
-          if (k < n) {
-            const long long at = static_cast<long long>(k ? 2 * (cta + k) : lead.x) * a.max_rows + r;
-            ml[i] = a.ml[at];
-            const float* src = a.part + at * D + lane * E;
+      for (int e = 0; e < E; ++e) x.o[e] = 0.f;
+      for (int k = 0; k < 8; ++k) {
+        const float f = ex2(sm[k].x - base);
+        x.l = fmaf(sm[k].y, f, x.l);
 #pragma unroll
-            for (int e = 0; e < E; e += 2) {
-              const float2 v = *reinterpret_cast<const float2*>(src + e);
-              x[i][e] = v.x, x[i][e + 1] = v.y;
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[i][e] = 0.f;
-          }
-        }
-        float top = m;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, ml[i].x);
-        if (top == -INFINITY) continue;            // rows that see nothing so far
-        const float f = ex2(m - top);
-        l *= f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] *= f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float w = ex2(ml[i].x - top);
-          l = fmaf(ml[i].y, w, l);
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = fmaf(x[i][e], w, o[e]);
-        }
-        m = top;
+        for (int e = 0; e < E; ++e) x.o[e] = fmaf(so[k][lane * E + e], f, x.o[e]);
       }
+      x.store(a, lead.w, where.x, where.y);
     }
-    if (per_row > 1) {                             // the same for the whole block
-      if (lane == 0) sm[warp] = make_float2(m, l);
-#pragma unroll
-      for (int e = 0; e < E; ++e) so[warp][lane * E + e] = o[e];
-      __syncthreads();
-      if (sub == 0) {
-        float top = m;
-        for (int k = 1; k < per_row; ++k) top = fmaxf(top, sm[warp + k].x);
-        if (top > -INFINITY) {
-          float f = ex2(m - top);
-          l *= f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] *= f;
-          for (int k = 1; k < per_row; ++k) {
-            f = ex2(sm[warp + k].x - top);
-            l += sm[warp + k].y * f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] += so[warp + k][lane * E + e] * f;
-          }
-        }
-      }
-      __syncthreads();
-    }
-    if (sub == 0 && r < rows) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int tr = r / a.group, tok = lead.w * a.tokens + tr, h = where.x * a.group + r - tr * a.group;
-      uint32_t* out = reinterpret_cast<uint32_t*>(a.o + static_cast<long long>(where.y + tok) * a.ldo + static_cast<long long>(h) * D + lane * E);
-#pragma unroll
-      for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16(o[e] * inv, o[e + 1] * inv);
-    }
+    __syncthreads();
   }
 }
 
@@ -967,7 +979,7 @@ cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tq1, const CUt
   cfg.dynamicSmemBytes = Lay<D>::kSmem;
   e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<D>, tq, tq1, tk, tv, a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(grid, std::min(kJoinY, a.max_rows));
+  cfg.gridDim = dim3(grid, kJoinY);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_parts<D>, a);
