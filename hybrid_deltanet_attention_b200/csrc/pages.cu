@@ -481,7 +481,8 @@ __device__ void remap_table(const mk_paged_cache& c) {
   }
 }
 
-// Page copies. A task is 2048 16-byte vectors of one page pair (8 in flight per thread); the
+// Page copies. A task is 512 16-byte vectors of one page pair (4 in flight per thread; small tasks, so that a few
+// pages still reach every SM: forking 8 pages of 1 MB 12.4 us, with tasks of 2048 vectors 14.5); the
 // vectors of a pair are numbered over (layer, K or V, head, slot, entry), entries innermost, so
 // a warp reads consecutive addresses whatever the strides.
 struct CopyArgs {
@@ -492,7 +493,7 @@ struct CopyArgs {
   int remap;                     // compaction: the table follows the pages
   int* err;
 };
-constexpr int kCopyThreads = 256, kCopyPer = 8;
+constexpr int kCopyThreads = 128, kCopyPer = 4;
 
 __global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant__ CopyArgs a) {
   if (a.count) asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while its plan still runs
@@ -541,11 +542,13 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant
   }
 }
 
-// Grid for at most `pairs` copies of whole pages.
-cudaError_t launch_copy(const CopyArgs& a, long long pairs, cudaStream_t s) {
+// Grid for at most `pairs` copies of whole pages, and at most `most` blocks an SM over the launch. Blocks beyond
+// what an SM holds even out the end of a large copy (357 MB: 70 us of 128 a SM, 80 of 4), but a call that usually
+// copies nothing should not pay for them.
+cudaError_t launch_copy(const CopyArgs& a, long long pairs, int most, cudaStream_t s) {
   const long long vec = 2ll * a.from.n_layers * a.from.kv_heads * a.from.page_size * (a.from.head_dim / 8);
-  const long long tasks = (vec + kCopyThreads * kCopyPer - 1) / (kCopyThreads * kCopyPer);
-  const long long grid = std::min<long long>(148 * 4, tasks > (148 * 4) / std::max(1ll, pairs) ? 148 * 4 : tasks * pairs);
+  const long long tasks = (vec + kCopyThreads * kCopyPer - 1) / (kCopyThreads * kCopyPer), cap = 148ll * most;
+  const long long grid = tasks > cap / std::max(1ll, pairs) ? cap : tasks * pairs;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, grid)));
   cfg.blockDim = dim3(kCopyThreads);
@@ -590,9 +593,9 @@ cudaError_t launch_plan(PlanKernel kernel, const mk_paged_cache& c, const int* a
   return cudaGetLastError();
 }
 
-cudaError_t copy_planned(const mk_paged_cache& c, long long pairs, int remap, cudaStream_t s) {
+cudaError_t copy_planned(const mk_paged_cache& c, long long pairs, int most, int remap, cudaStream_t s) {
   const Work w = work_of(c);
-  return launch_copy(CopyArgs{c, c, w.src, w.dst, w.rows, w.count, 0, remap, c.err}, pairs, s);
+  return launch_copy(CopyArgs{c, c, w.src, w.dst, w.rows, w.count, 0, remap, c.err}, pairs, most, s);
 }
 
 }  // namespace
@@ -613,7 +616,7 @@ extern "C" int mk_pages_resize(const mk_paged_cache* c, const int32_t* d_seqs, c
   if (!d_seqs) return mk::refuse(who, "NULL sequence ids");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = mk::launch_plan(mk::plan_resize, *c, d_seqs, d_lens, n, s);
-  if (e == cudaSuccess && d_lens) e = mk::copy_planned(*c, n, 0, s);   // freeing replaces no page
+  if (e == cudaSuccess && d_lens) e = mk::copy_planned(*c, n, 2, 0, s);   // freeing replaces no page
   return mk::done(who, e);
 }
 
@@ -626,7 +629,7 @@ extern "C" int mk_pages_fork(const mk_paged_cache* c, const int32_t* d_src, cons
   if (!d_src || !d_dst) return mk::refuse(who, "NULL sequence ids");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = mk::launch_plan(mk::plan_fork, *c, d_src, d_dst, n, s);
-  if (e == cudaSuccess) e = mk::copy_planned(*c, n, 0, s);
+  if (e == cudaSuccess) e = mk::copy_planned(*c, n, 128, 0, s);
   return mk::done(who, e);
 }
 
@@ -637,7 +640,7 @@ extern "C" int mk_pages_compact(const mk_paged_cache* c, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   mk::plan_compact<<<1, mk::kPlanThreads, 0, s>>>(*c);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = mk::copy_planned(*c, c->n_pages / 2 + 1, 1, s);
+  if (e == cudaSuccess) e = mk::copy_planned(*c, c->n_pages / 2 + 1, 64, 1, s);
   return mk::done(who, e);
 }
 
@@ -653,6 +656,6 @@ extern "C" int mk_pages_copy(const mk_paged_cache* from, const mk_paged_cache* t
   if (n < 0) return mk::refuse(who, "negative count");
   if (n == 0) return MK_OK;
   if (!d_src || !d_dst) return mk::refuse(who, "NULL page ids");
-  return mk::done(who, mk::launch_copy(mk::CopyArgs{*from, *to, d_src, d_dst, nullptr, nullptr, n, 0, to->err}, n,
+  return mk::done(who, mk::launch_copy(mk::CopyArgs{*from, *to, d_src, d_dst, nullptr, nullptr, n, 0, to->err}, n, 128,
                                        static_cast<cudaStream_t>(stream)));
 }

@@ -2,8 +2,9 @@
 // the pages of a cache, in one pass: every projection entry is read once and every result
 // written once, so many rows are bound by HBM and one row by the latency of its dependent loads.
 //
-// A warp takes up to eight heads of one row, fewer (down to one) when there are too few rows to fill
-// the GPU, and has the next head on its way while it works on one. A lane holds head_dim / 32 consecutive entries, so
+// A warp takes up to 32 heads of one row, fewer (down to one) when there are too few rows to fill
+// the GPU, and has the next head on its way while it works on one (4568 rows of 32 heads of 256: 43.5 us with up to 32
+// heads a warp, 46 with 16, 50 with 8, 58 with 4; four blocks of 256 threads an SM). A lane holds head_dim / 32 consecutive entries, so
 // loads and stores are one 8- to 32-byte vector a lane and the mean of squares is one warp sum. The
 // rotation partner of entry i is entry i + rot_dim / 2, which lies 16 rot_dim / head_dim lanes on
 // at the same place in the lane: one shuffle per entry. The angles of the row, position *
@@ -23,7 +24,7 @@
 namespace mk {
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 256;
 
 struct RopeArgs {
   int rows, hq, hkv, rot;
@@ -50,7 +51,7 @@ __device__ __forceinline__ void load_row(const float* p, float* x) {
   } else {
 #pragma unroll
     for (int i = 0; i < E; i += 4) {
-      const float4 t = *reinterpret_cast<const float4*>(p + i);
+      const float4 t = __ldcs(reinterpret_cast<const float4*>(p + i));
       x[i] = t.x, x[i + 1] = t.y, x[i + 2] = t.z, x[i + 3] = t.w;
     }
   }
@@ -98,10 +99,10 @@ __device__ __forceinline__ void turn_cs(int pos, double per, float& c, float& s)
   sincospif(static_cast<float>(2.0 * (t - rint(t))), &s, &c);
 }
 
-constexpr int kHeads = 8;   // heads of a warp, at most
+constexpr int kHeads = 32;   // heads of a warp, at most
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 4) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const long long task = blockIdx.x * static_cast<long long>(kRopeThreads / 32) + (threadIdx.x >> 5);
