@@ -308,6 +308,11 @@ __device__ __forceinline__ SeqWork shfl_work(const SeqWork& w, int src) {
   return SeqWork{__shfl_sync(0xFFFFFFFFu, w.row0, src), __shfl_sync(0xFFFFFFFFu, w.rows, src), __shfl_sync(0xFFFFFFFFu, w.pos0, src),
                  __shfl_sync(0xFFFFFFFFu, w.len, src),  __shfl_sync(0xFFFFFFFFu, w.seq, src),  __shfl_sync(0xFFFFFFFFu, w.row_tiles, src)};
 }
+__device__ __forceinline__ long long warp_sum64(long long v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
 // Units of one kv head of each lane's sequence: short ones by their lane, long ones by the warp.
 __device__ long long head_units(const AttnArgs& a, const SeqWork& w) {
   const int lane = threadIdx.x & 31;
@@ -317,17 +322,12 @@ __device__ long long head_units(const AttnArgs& a, const SeqWork& w) {
   for (unsigned big = __ballot_sync(0xFFFFFFFFu, w.row_tiles > 4); big; big &= big - 1) {
     const int src = __ffs(big) - 1;
     const SeqWork x = shfl_work(w, src);
-    int sum = 0;
+    long long sum = 0;
     for (int j = lane; j < x.row_tiles; j += 32) sum += extra_units(a, x, j) + key_tiles(a, x, j);
-    const int t = __reduce_add_sync(0xFFFFFFFFu, sum);
-    if (lane == src) u = t;
+    sum = warp_sum64(sum);
+    if (lane == src) u = sum;
   }
   return u;
-}
-__device__ __forceinline__ long long warp_sum64(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
 }
 __device__ __forceinline__ long long warp_scan64(long long v) {   // inclusive
 #pragma unroll
@@ -472,10 +472,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
         Segment s{};
         s.row0 = w.row0, s.new_rows = w.rows, s.pos0 = w.pos0, s.len = w.len, s.seq = w.seq;
         s.kvh = static_cast<int>(rel / h);
-        int rem = static_cast<int>(rel - s.kvh * h), tiles = 0;
+        long long rem = rel - s.kvh * h;           // units into this head
+        int tiles = 0;
         for (int j0 = 0;; j0 += 32) {              // the row tile that holds unit rem of this head
           const int t = j0 + lane < w.row_tiles ? extra_units(a, w, j0 + lane) + key_tiles(a, w, j0 + lane) : 0;
-          const int inc = static_cast<int>(warp_scan64(t));
+          const long long inc = warp_scan64(t);
           const unsigned hit = __ballot_sync(0xFFFFFFFFu, inc > rem);
           if (hit) {
             const int k = __ffs(hit) - 1;
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
         const int over = extra_units(a, w, s.tile);
         const int upto = static_cast<int>(min(static_cast<long long>(tiles), rem + (u1 - u)));
         u += upto - rem;
-        s.t0 = max(0, rem - over);
+        s.t0 = max(0, static_cast<int>(rem) - over);
         s.t1 = upto - over;
         if (s.t1 <= s.t0) continue;
         tiles -= over;

@@ -392,8 +392,8 @@ int mk_pages_copy(const mk_paged_cache* from, const mk_paged_cache* to, const in
  * (half split, as the model's attention; entries from rot_dim on are only normed). Norms and
  * rotation in fp32, angles in float64, one rounding to bf16 at the end.
  * With `cache`: rows seq_start[i] .. seq_start[i+1]-1 are the last
- * positions of sequence seqs[i] (or i, with seqs NULL), whose len already counts them (see
- * mk_pages_resize): row r has position len - seq_start[i+1] + r. Keys, and the values as they
+ * positions of sequence seqs[i] (or i, with seqs NULL; the sequences of a call differ), whose len already counts
+ * them (see mk_pages_resize): row r has position len - seq_start[i+1] + r. Keys, and the values as they
  * are, go to `layer` of the cache in bf16. Rows outside [seq_start[0], seq_start[n]) are left as
  * they are in q_out. A row whose position or page does not exist sets MK_DEVERR_BAD_PAGE, gets zero
  * queries and stores nothing. Without `cache`: positions gives each row's position (any int32), and

@@ -247,6 +247,95 @@ def test_attention_bad_pages_and_sequences():
     assert np.all(np.abs(f64(out[:1]) - o) <= ref.attention_bound(o, mag, big, 128 ** -0.5, 128))
 
 
+def test_attention_of_many_short_sequences():
+    """More sequences than one round of the kernel's lookup takes."""
+    rng = random.Random(4)
+    lens = [rng.randint(0, 40) for _ in range(1300)]
+    run_attention(11, lens, [min(n, rng.choice([0, 1, 1, 2])) for n in lens], 2, 1, 64, 8)
+
+
+def test_rows_before_and_between_sequences():
+    """The first sequence need not start at row 0; rows outside stay as they are."""
+    rng = np.random.default_rng(3)
+    c, table = make_cache(rng, [40, 70], 16, 2, 128)
+    x = torch.randn(20, 8, 128, device="cuda")
+    out = torch.full((20, 4, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    c.append(0, x[:, :4], x[:, 4:6], x[:, 6:], ints([7, 7, 12]), ints([0, 1]), out=out)
+    q = out.clone()
+    o = torch.full_like(out, 5.0)
+    c.attention(0, q, ints([7, 7, 12]), ints([0, 1]), out=o)
+    c.sync()
+    for t in (out, o):
+        assert (t[:7] == 5.0).all() and (t[12:] == 5.0).all() and (t[7:12] != 5.0).any()
+    k, v = gather(c.k, 0, table[1], 70, 16), gather(c.v, 0, table[1], 70, 16)
+    want, mag, big = ref.attention(f64(q[7:12]), k, v, np.arange(65, 70), 128 ** -0.5)
+    assert np.all(np.abs(f64(o[7:12]) - want) <= ref.attention_bound(want, mag, big, 128 ** -0.5, 128))
+
+
+def test_pages_further_apart_than_32_bits():
+    """Pages, layers and heads 2^31 entries and more from each other."""
+    m, far = hda(), (1 << 30) + 4096
+    big = [torch.empty(2 * far + far // 2 + 65536, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kv = [t.as_strided((2, 3, 1, 16, 128), (far // 2, far, 16 * 128, 128, 1)) for t in big]   # [layers][pages][heads][slots][d]
+    c = m.PagedCache(kv[0], kv[1], torch.full((3, 3), -1, dtype=torch.int32, device="cuda"), ints([0, 0, 0]), ints([0, 0, 0]))
+    c.resize(ints([0]), ints([8]))
+    c.resize(ints([1]), ints([8]))
+    c.free(ints([0]))
+    c.resize(ints([1]), ints([40]))                # pages 1, 0, 2
+    assert c.table[1].tolist() == [1, 0, 2]
+    for layer in range(2):
+        x = torch.randn(40, 6, 128, device="cuda")
+        q = c.append(layer, x[:, :4], x[:, 4:5], x[:, 5:], ints([0, 40]), ints([1]))
+        o = c.attention(layer, q, ints([0, 40]), ints([1]))
+        c.sync()
+        row = c.table[1].cpu().numpy()
+        k, v = gather(c.k, layer, row, 40, 16), gather(c.v, layer, row, 40, 16)
+        assert np.array_equal(v[:, 0], f64(x[:, 5].bfloat16()))
+        want, mag, s = ref.attention(f64(q), k, v, np.arange(40), 128 ** -0.5)
+        assert np.all(np.abs(f64(o) - want) <= ref.attention_bound(want, mag, s, 128 ** -0.5, 128))
+    c.copy_pages(ints([2]), ints([0]))
+    c.sync()
+    assert torch.equal(c.k[:, 0], c.k[:, 2]) and torch.equal(c.v[:, 0], c.v[:, 2])
+
+
+def test_two_calls_at_once():
+    """Two caches worked on in two streams at the same time, eager and captured."""
+    rng = np.random.default_rng(5)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    work, want = [], []
+    for i in range(2):
+        c, table = make_cache(rng, [3000 + i, 77], 16, 2, 128)
+        q = torch.randn(90, 8, 128, device="cuda").bfloat16()
+        start = ints([0, 60, 90])
+        work.append((c, q, start))
+        want.append(c.attention(0, q, start))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (c, q, start) in enumerate(work):
+            got[i].append(c.attention(0, q, start, stream=streams[i]))
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c, q, start in work:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c.attention(0, q, start))
+        graphs.append(g)
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for i, g in enumerate(graphs):
+            with torch.cuda.stream(streams[i]):
+                g.replay()
+        torch.cuda.synchronize()
+        for i in range(2):
+            got[i].append(outs[i].clone())
+    for i in range(2):
+        work[i][0].sync()
+        assert all(torch.equal(o, want[i]) for o in got[i])
+
+
 def test_attention_is_the_same_every_time():
     lens, new = [3000, 17, 900, 1, 250], [1, 17, 33, 1, 250]
     a, _ = run_attention(4, lens, new, 8, 2, 256, 32)
