@@ -299,8 +299,9 @@ __device__ __forceinline__ int key_tiles(const AttnArgs& a, const SeqWork& w, in
   const int keys = w.pos0 + min((j + 1) * a.tokens, w.rows);
   return max(1, (keys + kN - 1) / kN);
 }
-// What row tile j costs beside its key tiles, in units of them: measured at about 3 key tiles for 128 rows
-// of 256 entries and 6 of 128 (the products of 256 take twice as long), next to nothing for a few rows.
+// What row tile j costs beside its key tiles, in units of them (a.over + 1 for 128 rows, 1 for a few). Measured, 256
+// entries: a 4096-token prompt 79 us with 3 units, 81 with 2 and 80 with 4; 128 entries, ragged chunks: 68 us with 4, 69 with 3
+// and 5.
 __device__ __forceinline__ int extra_units(const AttnArgs& a, const SeqWork& w, int j) {
   return 1 + min(a.tokens, w.rows - j * a.tokens) * a.group * a.over / kM;
 }
@@ -702,7 +703,12 @@ __global__ void __launch_bounds__(kThreads_, 1)
           for (int c = 0; c < kN; c += 32) tmem_wait_ld(x + c);
           if (masked) {
 #pragma unroll
-            for (int c = 0; c < kN; ++c) x[c] = key0 + c <= pos ? x[c] : -INFINITY;
+            for (int w = 0; w < kN / 32; ++w) {
+              const int see = min(32, max(0, pos + 1 - key0 - 32 * w));   // visible columns of these 32
+              const uint32_t bits = see >= 32 ? 0xFFFFFFFFu : (1u << see) - 1u;
+#pragma unroll
+              for (int c = 0; c < 32; ++c) x[32 * w + c] = bits >> c & 1 ? x[32 * w + c] : -INFINITY;
+            }
           }
           float m0 = -INFINITY, m1 = m0, m2 = m0, m3 = m0;
 #pragma unroll
@@ -1061,7 +1067,7 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
     const float c2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1e-30f);
     const mk::AttnArgs a{*c, layer, rows, q_heads, q_heads / c->kv_heads, box, static_cast<const uint16_t*>(d_q), ldq,
                          static_cast<uint16_t*>(d_out), ldo, mk::kM / (q_heads / c->kv_heads),
-                         std::min(mk::kM / (q_heads / c->kv_heads), (rows + n - 1) / n), c->head_dim == 256 ? 2 : c->head_dim == 128 ? 4 : 6, c2, scale < 0 ? 1 : 0,
+                         std::min(mk::kM / (q_heads / c->kv_heads), (rows + n - 1) / n), c->head_dim == 256 ? 2 : c->head_dim == 128 ? 3 : 5, c2, scale < 0 ? 1 : 0,
                          mk::NewRows{d_seq_start, d_seqs, n}, reinterpret_cast<float*>(ws), reinterpret_cast<float2*>(ws + sc.ml),
                          reinterpret_cast<int4*>(ws + sc.lead), max_rows};
     CUtensorMap tq, tq1, tk, tv;
