@@ -7,10 +7,11 @@ rotation without a cache. Argument checks and marshalling only; every step runs 
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 import struct
-from typing import Callable, Optional, Tuple
+from typing import Optional, Tuple
 
 import torch
 
@@ -19,7 +20,9 @@ from ._abi import MkPagedCache, MkQkRope, check
 
 _DTYPES = {torch.float32: _abi.MK_DT_F32, torch.bfloat16: _abi.MK_DT_BF16}
 _BF16 = torch.bfloat16
+_load_library = _abi.load_library
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
 # mk_qk_rope in one piece (filling a ctypes structure field by field costs more than the call)
 _ROPE = struct.Struct("@6idf4xPqPqPqPPPqPqPPiiPP")
 assert _ROPE.size == C.sizeof(MkQkRope)
@@ -30,17 +33,37 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _run(device: torch.device, stream: Optional[torch.cuda.Stream], body: Callable):
-    """body(raw stream) with the tensors' device current, on `stream` or the device's current stream, so that
-    what it allocates belongs to that stream. The usual case (the current device and stream) pays for no context."""
+class _Here:
+    """The tensors' device and its current stream are current already: the raw stream, and nothing to undo."""
+    __slots__ = ("raw",)
+
+    def __init__(self, raw: int):
+        self.raw = raw
+
+    def __enter__(self) -> int:
+        return self.raw
+
+    def __exit__(self, *exc) -> None:
+        return None
+
+
+@contextlib.contextmanager
+def _there(device: torch.device, stream: Optional[torch.cuda.Stream]):
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            return body(_raw_stream(device.index))
         with torch.cuda.device(device):
-            return body(_raw_stream(device.index))
-    _need(stream.device == device, f"the stream is on {stream.device}, the tensors on {device}")
-    with torch.cuda.stream(stream):
-        return body(stream.cuda_stream)
+            yield _raw_stream(device.index)
+    else:
+        _need(stream.device == device, f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+
+
+def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
+    """A context with the tensors' device current, on `stream` or the device's current stream, so that what is
+    allocated in it belongs to that stream; gives the raw stream. The usual case costs next to nothing."""
+    if stream is None and _current_device() == device.index:
+        return _Here(_raw_stream(device.index))
+    return _there(device, stream)
 
 
 # Tensors are compared by device index here: every caller has made sure that the index means CUDA.
@@ -106,7 +129,8 @@ class PagedCache:
         self._p, self._address = C.byref(c), C.addressof(c)
         self._d, self._kv_heads, self._n_seqs = c.head_dim, c.kv_heads, c.n_seqs
         self._scale = 1.0 / math.sqrt(c.head_dim)
-        self._scratch = (-1, -1, 0)
+        self._scratch, self._scratch_for = 0, None
+        self._attention = self.lib.mk_paged_attention
         self._bytes = torch.empty(0, dtype=torch.uint8, device=k.device)
 
     @classmethod
@@ -127,25 +151,29 @@ class PagedCache:
         self._movable()
         s, l = _ints(seqs, "seqs", self._index), _ints(lens, "lens", self._index)   # noqa: E741
         _need(seqs.numel() == lens.numel(), "seqs and lens differ in length")
-        _run(self.device, stream, lambda st: check(self.lib.mk_pages_resize(self._p, s, l, seqs.numel(), st)))
+        with _on(self.device, stream) as st:
+            check(self.lib.mk_pages_resize(self._p, s, l, seqs.numel(), st))
 
     def free(self, seqs: torch.Tensor, stream=None) -> None:
         """Give back every page of these sequences."""
         self._movable()
         s = _ints(seqs, "seqs", self._index)
-        _run(self.device, stream, lambda st: check(self.lib.mk_pages_resize(self._p, s, None, seqs.numel(), st)))
+        with _on(self.device, stream) as st:
+            check(self.lib.mk_pages_resize(self._p, s, None, seqs.numel(), st))
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Make sequence dst[i] a continuation of src[i], sharing its full pages (mk_pages_fork)."""
         self._movable()
         a, b = _ints(src, "src", self._index), _ints(dst, "dst", self._index)
         _need(src.numel() == dst.numel(), "src and dst differ in length")
-        _run(self.device, stream, lambda st: check(self.lib.mk_pages_fork(self._p, a, b, src.numel(), st)))
+        with _on(self.device, stream) as st:
+            check(self.lib.mk_pages_fork(self._p, a, b, src.numel(), st))
 
     def compact(self, stream=None) -> None:
         """Move the used pages to the lowest ids (mk_pages_compact)."""
         self._movable()
-        _run(self.device, stream, lambda st: check(self.lib.mk_pages_compact(self._p, st)))
+        with _on(self.device, stream) as st:
+            check(self.lib.mk_pages_compact(self._p, st))
 
     def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, source: Optional["PagedCache"] = None, stream=None) -> None:
         """Copy page src[i] of `source` (or of this cache) to page dst[i] of this cache (mk_pages_copy)."""
@@ -153,7 +181,8 @@ class PagedCache:
         _need(f.device == self.device, "the caches are on different devices")
         a, b = _ints(src, "src", self._index), _ints(dst, "dst", self._index)
         _need(src.numel() == dst.numel(), "src and dst differ in length")
-        _run(self.device, stream, lambda st: check(self.lib.mk_pages_copy(f._p, self._p, a, b, src.numel(), st)))
+        with _on(self.device, stream) as st:
+            check(self.lib.mk_pages_copy(f._p, self._p, a, b, src.numel(), st))
 
     # ---- new tokens ----
     def append(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_start: torch.Tensor,
@@ -170,24 +199,28 @@ class PagedCache:
                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Causal attention of new rows over their sequences' pages (mk_paged_attention); q bfloat16
         [rows][query heads][head dim], scale 1/sqrt(head dim) unless given. Returns bfloat16 like q."""
-        index, rows = self._index, q.shape[0]
-        qp, ldq, hq = _heads(q, "q", index, _BF16, rows, self._d)
+        index, rows, d = self._index, q.shape[0], self._d
+        qp, ldq, hq = _heads(q, "q", index, _BF16, rows, d)
         start, ids, n = _new_rows(seq_start, seqs, self._n_seqs, index)
         if out is not None:
-            op, ldo, ho = _heads(out, "out", index, _BF16, rows, self._d)
+            op, ldo, ho = _heads(out, "out", index, _BF16, rows, d)
             _need(ho == hq, "out must have q's shape")
-
-        def body(st):
-            o, p, ld = (out, op, ldo) if out is not None else (torch.empty_like(q), 0, hq * self._d)
-            if self._scratch[:2] != (rows, hq):      # bytes for calls of this shape
-                self._scratch = (rows, hq, max(32, self.lib.mk_paged_attention_scratch(self._p, rows, hq)))
-            size = self._scratch[2]
+        else:
+            op, ldo = 0, hq * d
+        if self._scratch_for != (rows, hq):          # bytes for calls of this shape
+            self._scratch = max(32, self.lib.mk_paged_attention_scratch(self._p, rows, hq))
+            self._scratch_for = (rows, hq)
+        with _on(self.device, stream) as st:
+            if out is None:
+                out = torch.empty_like(q)
+                op = out.data_ptr()
+            size = self._scratch
             scratch = self._bytes.new_empty(size)
-            check(self.lib.mk_paged_attention(self._p, layer, qp, ldq, rows, hq, start, ids, n, self._scale if scale is None else scale,
-                                              p or o.data_ptr(), ld, scratch.data_ptr(), size, st))
-            return o
-
-        return _run(self.device, stream, body)
+            rc = self._attention(self._p, layer, qp, ldq, rows, hq, start, ids, n, self._scale if scale is None else scale, op, ldo,
+                                 scratch.data_ptr(), size, st)
+        if rc:
+            check(rc)
+        return out
 
     def sync(self, stream=None) -> None:
         """Wait for the stream and raise if a call found bad ids, lengths or too few pages (the word is then cleared)."""
@@ -238,17 +271,20 @@ def _rope(dev, q, k, v, positions, q_gain, k_gain, eps, theta, rot_dim, q_out, k
     gq = 0 if q_gain is None else _gain(q_gain, index, d)
     gk = 0 if k_gain is None else _gain(k_gain, index, d)
 
-    def body(st):
+    with _on(dev, stream) as st:
         # a fresh output is contiguous: the heads of a row are, and rows that are further apart are packed
-        qo = q_out if q_out is not None else torch.empty_like(q, dtype=_BF16)
-        ko = k_out if k_out is not None or cache is not None else torch.empty_like(k, dtype=_BF16)
-        a = _ROPE.pack(dt, rows, hq, hkv, d, d if rot_dim is None else rot_dim, theta, eps, qp, ldq, kp, ldk, vp, ldv, gq, gk,
-                       qop or qo.data_ptr(), ldqo, 0 if cache is not None else kop or ko.data_ptr(), ldko, pos, cp, layer, n, start,
-                       ids or 0)
-        check(_abi.load_library().mk_qk_norm_rope(a, st))
-        return qo, ko
-
-    return _run(dev, stream, body)
+        if q_out is None:
+            q_out = torch.empty_like(q, dtype=_BF16)
+            qop = q_out.data_ptr()
+        if cache is None and k_out is None:
+            k_out = torch.empty_like(k, dtype=_BF16)
+            kop = k_out.data_ptr()
+        rc = _load_library().mk_qk_norm_rope(
+            _ROPE.pack(dt, rows, hq, hkv, d, d if rot_dim is None else rot_dim, theta, eps, qp, ldq, kp, ldk, vp, ldv, gq, gk, qop, ldqo,
+                       kop, ldko, pos, cp, layer, n, start, ids or 0), st)
+    if rc:
+        check(rc)
+    return q_out, k_out
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, *, q_gain: Optional[torch.Tensor] = None,
