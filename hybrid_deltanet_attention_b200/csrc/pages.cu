@@ -481,10 +481,10 @@ __device__ void remap_table(const mk_paged_cache& c) {
   }
 }
 
-// Page copies. A task is 512 16-byte vectors of one page pair (4 in flight per thread; small tasks, so that a few
-// pages still reach every SM: forking 8 pages of 1 MB 12.4 us, with tasks of 2048 vectors 14.5); the
-// vectors of a pair are numbered over (layer, K or V, head, slot, entry), entries innermost, so
-// a warp reads consecutive addresses whatever the strides.
+// Page copies. A warp's task is up to 256 16-byte vectors of one (page pair, layer, K or V, head), 8 in flight a
+// lane: the two divisions that find it are paid once, inside it an address is a shift and a product whatever the
+// strides (divisions for every vector made the copy bound by instructions: 70 % of the issue slots), and a few
+// pages still reach every SM.
 struct CopyArgs {
   mk_paged_cache from, to;
   const int *src, *dst, *rows;   // rows null: whole pages
@@ -493,7 +493,7 @@ struct CopyArgs {
   int remap;                     // compaction: the table follows the pages
   int* err;
 };
-constexpr int kCopyThreads = 128, kCopyPer = 4;
+constexpr int kCopyThreads = 128, kCopyWarps = kCopyThreads / 32, kCopyVec = 256, kCopyPer = 8;
 
 __global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant__ CopyArgs a) {
   if (a.count) asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while its plan still runs
@@ -501,44 +501,38 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant
   const mk_paged_cache& t = a.to;
   const int count = a.count ? *a.count : a.n;
   if (a.remap && count > 0) remap_table(f);
-  const int dv = f.head_dim / 8, sh = __ffs(dv) - 1;   // vectors of a row (a power of two)
-  const unsigned per_max = static_cast<unsigned>(f.n_layers) * 2u * f.kv_heads;   // (layer, K or V, head) triples
-  const unsigned page_tasks = (per_max * f.page_size * dv + kCopyThreads * kCopyPer - 1) / (kCopyThreads * kCopyPer);
-  for (unsigned long long task = blockIdx.x; task < static_cast<unsigned long long>(page_tasks) * count; task += gridDim.x) {
+  const int dv = f.head_dim / 8, sh = __ffs(dv) - 1, lane = threadIdx.x & 31;   // vectors of a row (a power of two)
+  const unsigned triples = static_cast<unsigned>(f.n_layers) * 2u * f.kv_heads;
+  const unsigned chunks = (static_cast<unsigned>(f.page_size) * dv + kCopyVec - 1) / kCopyVec;   // of a triple's page
+  const unsigned page_tasks = triples * chunks;   // below 2^31 (checked by the host)
+  for (unsigned long long task = blockIdx.x * static_cast<unsigned long long>(kCopyWarps) + (threadIdx.x >> 5);
+       task < static_cast<unsigned long long>(page_tasks) * count; task += static_cast<unsigned long long>(gridDim.x) * kCopyWarps) {
     const int pair = static_cast<int>(task / page_tasks);
+    const unsigned in = static_cast<unsigned>(task - static_cast<unsigned long long>(pair) * page_tasks);
     const int ps = a.src[pair], pd = a.dst[pair];
-    const unsigned rows = a.rows ? a.rows[pair] : f.page_size;
-    const unsigned total = per_max * rows * dv;   // below 2^31 (checked by the host)
-    const unsigned v0 = static_cast<unsigned>(task - static_cast<unsigned long long>(pair) * page_tasks) * (kCopyThreads * kCopyPer) +
-                        threadIdx.x;
+    const unsigned total = static_cast<unsigned>(a.rows ? a.rows[pair] : f.page_size) * dv;   // vectors of a triple
     if (ps < 0 || ps >= f.n_pages || pd < 0 || pd >= t.n_pages) {
-      if (threadIdx.x == 0) atomicOr(a.err, MK_DEVERR_BAD_PAGE);
+      if (lane == 0) atomicOr(a.err, MK_DEVERR_BAD_PAGE);
       continue;
     }
-    uint4 x[kCopyPer];
-    uint4* to[kCopyPer];
+    const unsigned triple = in / chunks, v0 = (in - triple * chunks) * kCopyVec, lk = triple / f.kv_heads;
+    const int h = static_cast<int>(triple - lk * f.kv_heads), layer = static_cast<int>(lk >> 1);
+    const bool val = lk & 1;
+    const uint16_t* s = static_cast<const uint16_t*>(val ? f.v : f.k) + layer * f.layer_stride + ps * f.page_stride + h * f.head_stride;
+    uint16_t* d = static_cast<uint16_t*>(val ? t.v : t.k) + layer * t.layer_stride + pd * t.page_stride + h * t.head_stride;
+    for (unsigned v = v0 + lane; v < min(total, v0 + kCopyVec); v += 32 * kCopyPer) {
+      uint4 x[kCopyPer];
 #pragma unroll
-    for (int j = 0; j < kCopyPer; ++j) {
-      const unsigned v = v0 + j * kCopyThreads;
-      to[j] = nullptr;
-      if (v < total) {
-        const unsigned row = v >> sh, triple = row / rows, lk = triple / f.kv_heads;
-        const int e = static_cast<int>(v & (dv - 1)) * 8;
-        const int slot = static_cast<int>(row - triple * rows);
-        const int h = static_cast<int>(triple - lk * f.kv_heads);
-        const int layer = static_cast<int>(lk >> 1);
-        const bool val = lk & 1;
-        const uint16_t* s = static_cast<const uint16_t*>(val ? f.v : f.k) + layer * f.layer_stride + ps * f.page_stride +
-                            h * f.head_stride + slot * f.slot_stride + e;
-        uint16_t* d = static_cast<uint16_t*>(val ? t.v : t.k) + layer * t.layer_stride + pd * t.page_stride +
-                      h * t.head_stride + slot * t.slot_stride + e;
-        x[j] = *reinterpret_cast<const uint4*>(s);
-        to[j] = reinterpret_cast<uint4*>(d);
+      for (int j = 0; j < kCopyPer; ++j) {
+        const unsigned w = v + 32 * j;
+        if (w < total) x[j] = *reinterpret_cast<const uint4*>(s + (w >> sh) * f.slot_stride + (w & (dv - 1)) * 8);
+      }
+#pragma unroll
+      for (int j = 0; j < kCopyPer; ++j) {
+        const unsigned w = v + 32 * j;
+        if (w < total) *reinterpret_cast<uint4*>(d + (w >> sh) * t.slot_stride + (w & (dv - 1)) * 8) = x[j];
       }
     }
-#pragma unroll
-    for (int j = 0; j < kCopyPer; ++j)
-      if (to[j]) *to[j] = x[j];
   }
 }
 
@@ -546,8 +540,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant
 // what an SM holds even out the end of a large copy (357 MB: 70 us of 128 a SM, 80 of 4), but a call that usually
 // copies nothing should not pay for them.
 cudaError_t launch_copy(const CopyArgs& a, long long pairs, int most, cudaStream_t s) {
-  const long long vec = 2ll * a.from.n_layers * a.from.kv_heads * a.from.page_size * (a.from.head_dim / 8);
-  const long long tasks = (vec + kCopyThreads * kCopyPer - 1) / (kCopyThreads * kCopyPer), cap = 148ll * most;
+  const long long chunks = (static_cast<long long>(a.from.page_size) * (a.from.head_dim / 8) + kCopyVec - 1) / kCopyVec;
+  const long long tasks = (2ll * a.from.n_layers * a.from.kv_heads * chunks + kCopyWarps - 1) / kCopyWarps, cap = 148ll * most;
   const long long grid = tasks > cap / std::max(1ll, pairs) ? cap : tasks * pairs;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(std::max(1ll, grid)));
