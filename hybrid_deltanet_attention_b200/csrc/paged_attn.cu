@@ -21,6 +21,12 @@
 // box is the largest power of two of slots that divides the page size, at most 128); the order
 // K0 K1 V0 K2 V1 ... is the order of use, and it runs on across row tiles, so memory stays busy through
 // softmax and epilogue. Values are taken as they lie in the page (transposed by the MMA descriptor).
+//
+// Measured on a B200, per call: one token of each of 64 sequences (1.27 GB of keys and values) 203 us, 95 % of the
+// measured copy bandwidth; a 4096-token prompt (8/2 heads of 256) 79 us, 870 TFLOP/s of causal work, where
+// shared memory bounds a tile (128 x 128 tiles at 256 entries move 320 KB through it, 2560 clocks; measured 3400);
+// ragged chunks of 128-wide heads 70 us, bound by the chain of a group's softmax (about 3000 clocks a
+// tile, two groups at work); one token over 32769 positions 25 us, of which the stream of 67 MB is half.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
