@@ -45,6 +45,7 @@ namespace {
 constexpr int kM = 128, kN = 128;        // rows and keys of a tile
 constexpr int kSoftWarps = 8;
 constexpr int kThreads_ = 384;
+constexpr int kSoftRegs = 208, kOtherRegs = 88;
 constexpr int kSegs = 4;                 // segments the scheduler runs ahead
 constexpr float kRaise = 8.0f;           // log2 units
 constexpr uint64_t kWaitNs = 1000000000ull;
@@ -430,9 +431,9 @@ __global__ void __launch_bounds__(kThreads_, 1)
   tc::fence_proxy_async_smem();
   __syncthreads();   // the ring is the producers' from here
   const uint32_t tmem = b->tmem;
-  // registers: 256 x 208 + 128 x 88 = 384 x 168, what the CTA was launched with
+  // registers: 256 x 208 + 128 x 88 = 384 x 168, what the CTA was launched with (checked by the host)
   if (warp >= kSoftWarps) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == 10) {
     // ---- scheduler: cut [u0, u1) into segments
     int emitted = 0, made = 0, with_queries = 0;
@@ -665,7 +666,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
     __syncwarp();
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---- softmax and epilogue: thread = row r of the tile; the warps of group 0 take the even key
     // tiles of the CTA, those of group 1 the odd ones, so one group exponentiates while the other
     // loads the next scores and finds their maximum. m passes from tile to tile through shared
@@ -976,6 +977,11 @@ template <int D>
 cudaError_t launch_attn(const CUtensorMap& tq, const CUtensorMap& tq1, const CUtensorMap& tk, const CUtensorMap& tv, const AttnArgs& a, int grid, cudaStream_t s) {
   static std::atomic<uint64_t> attr_set{0};   // per device
   cudaError_t e = once_per_device(attr_set, [] {
+    // the register split must fit what a CTA is launched with: a larger one would wait for ever
+    cudaFuncAttributes f{};
+    const cudaError_t got = cudaFuncGetAttributes(&f, paged_attn_kernel<D>);
+    if (got != cudaSuccess) return got;
+    if (f.numRegs * kThreads_ < kSoftWarps * 32 * kSoftRegs + (kThreads_ - kSoftWarps * 32) * kOtherRegs) return cudaErrorInvalidConfiguration;
     return cudaFuncSetAttribute(paged_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kSmem);
   });
   if (e != cudaSuccess) return e;

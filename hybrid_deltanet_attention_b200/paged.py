@@ -66,6 +66,14 @@ def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
     return _there(device, stream)
 
 
+def _used_on(stream: Optional[torch.cuda.Stream], *tensors: Optional[torch.Tensor]) -> None:
+    """Arguments of a call on a stream that was given: their memory is not reused before it has run there."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 # Tensors are compared by device index here: every caller has made sure that the index means CUDA.
 def _ints(t: torch.Tensor, what: str, index: int) -> int:
     if t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != index or not t.is_contiguous():
@@ -153,6 +161,7 @@ class PagedCache:
         _need(seqs.numel() == lens.numel(), "seqs and lens differ in length")
         with _on(self.device, stream) as st:
             check(self.lib.mk_pages_resize(self._p, s, l, seqs.numel(), st))
+        _used_on(stream, seqs, lens)
 
     def free(self, seqs: torch.Tensor, stream=None) -> None:
         """Give back every page of these sequences."""
@@ -160,6 +169,7 @@ class PagedCache:
         s = _ints(seqs, "seqs", self._index)
         with _on(self.device, stream) as st:
             check(self.lib.mk_pages_resize(self._p, s, None, seqs.numel(), st))
+        _used_on(stream, seqs)
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
         """Make sequence dst[i] a continuation of src[i], sharing its full pages (mk_pages_fork)."""
@@ -168,6 +178,7 @@ class PagedCache:
         _need(src.numel() == dst.numel(), "src and dst differ in length")
         with _on(self.device, stream) as st:
             check(self.lib.mk_pages_fork(self._p, a, b, src.numel(), st))
+        _used_on(stream, src, dst)
 
     def compact(self, stream=None) -> None:
         """Move the used pages to the lowest ids (mk_pages_compact)."""
@@ -183,6 +194,7 @@ class PagedCache:
         _need(src.numel() == dst.numel(), "src and dst differ in length")
         with _on(self.device, stream) as st:
             check(self.lib.mk_pages_copy(f._p, self._p, a, b, src.numel(), st))
+        _used_on(stream, src, dst)
 
     # ---- new tokens ----
     def append(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_start: torch.Tensor,
@@ -220,6 +232,7 @@ class PagedCache:
                                  scratch.data_ptr(), size, st)
         if rc:
             check(rc)
+        _used_on(stream, q, seq_start, seqs, out)
         return out
 
     def sync(self, stream=None) -> None:
@@ -284,6 +297,7 @@ def _rope(dev, q, k, v, positions, q_gain, k_gain, eps, theta, rot_dim, q_out, k
                        kop, ldko, pos, cp, layer, n, start, ids or 0), st)
     if rc:
         check(rc)
+    _used_on(stream, q, k, v, positions, q_gain, k_gain, q_out, k_out, seq_start, seqs)
     return q_out, k_out
 
 

@@ -636,6 +636,36 @@ def test_captured_calls_follow_lengths_and_tables():
             assert np.all(np.abs(f64(go[i:i + 1]) - want) <= ref.attention_bound(want, mag, big, 128 ** -0.5, 128))
 
 
+def test_captured_page_calls():
+    """Fork, resize and compaction captured once and replayed on changed lists."""
+    c = hda().PagedCache.empty(2, 60, 2, 8, 64, 6, 8)
+    p = ref.Pages(60, 6, 8, 8)
+    src, dst, seqs, lens = ints([0]), ints([1]), ints([0, 2]), ints([0, 0])
+    c.fork(src, dst)                               # loads the kernels before the capture
+    c.resize(seqs, lens)
+    c.compact()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.resize(seqs, lens)
+        c.fork(src, dst)
+        c.compact()
+    rng = random.Random(3)
+    for step in range(12):
+        ids = rng.sample(range(6), 2)
+        new = [rng.randint(0, 40), rng.randint(0, 40)]
+        a, b = rng.sample(range(6), 2)
+        for t, v in ((seqs, ids), (lens, new), (src, [a]), (dst, [b])):
+            t.copy_(ints(v))
+        for q in range(60):
+            p.slot[q] = (np.arange(8) + 8 * q + step) % 251
+        signature(c, p)
+        g.replay()
+        c.sync()
+        assert p.resize(ids, new) and p.fork([a], [b])
+        p.compact()
+        same(c, p)
+
+
 def test_calls_on_another_stream():
     s = torch.cuda.Stream()
     rng = np.random.default_rng(2)
