@@ -6,8 +6,8 @@
 // CTA needs no grid-wide barrier between its phases. A copy kernel then moves the listed pages
 // with 16-byte loads and stores over the whole GPU, bound by HBM.
 //
-// Measured: a plan for 61 sequences in 16384 pages 9 us (about 16000 clocks: four dependent loads 4000, counts in
-// and out 3000, releases 2000, free list 5000, table 3000), for a fork of eight 1001-position sequences 7; the copies of
+// Measured: a plan for 61 sequences in 16384 pages about 7 us (dependent loads 4000 clocks, counts into shared memory
+// 1000, releases 2000, free list 4000, table 3000), for a fork of eight 1001-position sequences 6; the copies of
 // a 357 MB compaction 58 us, 6.2 TB/s.
 //
 // All decisions are order-free: releases and counts are integer atomics, pages are taken by
@@ -70,85 +70,75 @@ __device__ T block_scan(T v, T* total, T* red) {
 
 // The use counts and the list of free pages while a plan works on them: copies in shared memory for up
 // to kRefCached / kListCached pages (scattered counts, and entries that are read right after they were
-// written, each cost an L2 round trip otherwise), the arrays themselves beyond that.
+// written, each cost an L2 round trip otherwise), the arrays themselves beyond that. Changes go to the copy and,
+// without waiting, to the array, so nothing is written back at the end.
 constexpr int kRefCached = 48 * 1024, kListCached = 24 * 1024;
 struct Counts {
-  int* p;
+  int* p;          // to read from
+  int* all;        // the cache's counts
   int n;
   bool cached;
   __device__ int at(long long i) const { return cached ? p[i] : __ldcg(p + i); }
+  __device__ void add(int i, int by) const {
+    if (cached) atomicAdd(p + i, by);
+    atomicAdd(all + i, by);
+  }
+  __device__ void take(int i) const {   // a free page
+    if (cached) p[i] = 1;
+    all[i] = 1;
+  }
 };
 // Asynchronous: cp_async_wait and a barrier before the first use.
 __device__ Counts open_counts(const mk_paged_cache& c, int* cache) {
-  if (c.n_pages > kRefCached) return Counts{c.ref, c.n_pages, false};
+  if (c.n_pages > kRefCached) return Counts{c.ref, c.ref, c.n_pages, false};
   const bool wide = (reinterpret_cast<uintptr_t>(c.ref) & 15) == 0;
   const int quads = wide ? c.n_pages / 4 : 0;
   for (int i = threadIdx.x; i < quads; i += kPlanThreads) cp_async16(cache + 4 * i, c.ref + 4 * i, 16);
   for (int i = 4 * quads + threadIdx.x; i < c.n_pages; i += kPlanThreads) cp_async4(cache + i, c.ref + i, 4);
   cp_async_commit();
-  return Counts{cache, c.n_pages, true};
-}
-// After the block's last change (and a barrier).
-__device__ void close_counts(const mk_paged_cache& c, const Counts& r) {
-  if (!r.cached) return;
-  const bool wide = (reinterpret_cast<uintptr_t>(c.ref) & 15) == 0;
-  const int quads = wide ? c.n_pages / 4 : 0;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < quads; i += kPlanThreads) reinterpret_cast<int4*>(c.ref)[i] = reinterpret_cast<const int4*>(r.p)[i];
-  for (int i = 4 * quads + threadIdx.x; i < c.n_pages; i += kPlanThreads) c.ref[i] = r.p[i];
+  return Counts{cache, c.ref, c.n_pages, true};
 }
 
 // Ranks the free pages in ascending order into list until `want` are found; returns how many
-// there are (at most about want + one chunk are looked at). A lane looks at four consecutive counts at a
-// time, two such steps to a chunk of 8192 pages.
+// there are (at most about want + one chunk are looked at). A lane looks at four consecutive counts, the block at
+// 4096: most calls find their few pages in the first chunk.
 template <bool kCachedCounts>
 __device__ int list_free(const Counts& ref, int want, int* list, int* red) {
-  constexpr int kSteps = 2;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned below = (1u << lane) - 1u;
   const bool wide = kCachedCounts || (reinterpret_cast<uintptr_t>(ref.p) & 15) == 0;
   int found = 0;
-  for (long long base = 0; base < ref.n && found < want; base += kPlanThreads * 4 * kSteps) {
-    const int p0 = static_cast<int>(base) + warp * 128 * kSteps + lane * 4;   // below 2^31: n_pages is an int
-    unsigned mine[kSteps], before[kSteps], all[kSteps];
+  for (long long base = 0; base < ref.n && found < want; base += kPlanThreads * 4) {
+    const long long p = base + 4 * threadIdx.x;
+    int4 v = make_int4(1, 1, 1, 1);
+    if (wide && p + 4 <= ref.n) {
+      v = kCachedCounts ? *reinterpret_cast<const int4*>(ref.p + p) : __ldcg(reinterpret_cast<const int4*>(ref.p + p));
+    } else {
+      if (p < ref.n) v.x = ref.at(p);
+      if (p + 1 < ref.n) v.y = ref.at(p + 1);
+      if (p + 2 < ref.n) v.z = ref.at(p + 2);
+      if (p + 3 < ref.n) v.w = ref.at(p + 3);
+    }
+    const unsigned mine = (v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3;
+    unsigned before = 0, all = 0;                // free pages of the warp's lanes below, and of the warp
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const int p = p0 + 128 * k;
-      int4 v = make_int4(1, 1, 1, 1);
-      if (wide && p <= ref.n - 4) {
-        v = kCachedCounts ? *reinterpret_cast<const int4*>(ref.p + p) : __ldcg(reinterpret_cast<const int4*>(ref.p + p));
-      } else if (p >= 0) {
-        if (p < ref.n) v.x = ref.at(p);
-        if (p < ref.n - 1) v.y = ref.at(p + 1);
-        if (p < ref.n - 2) v.z = ref.at(p + 2);
-        if (p < ref.n - 3) v.w = ref.at(p + 3);
-      }
-      mine[k] = (v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3;
-      before[k] = all[k] = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const unsigned b = __ballot_sync(0xFFFFFFFFu, mine[k] >> j & 1);
-        before[k] += __popc(b & below);
-        all[k] += __popc(b);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const unsigned b = __ballot_sync(0xFFFFFFFFu, mine >> j & 1);
+      before += __popc(b & below);
+      all += __popc(b);
     }
     __syncthreads();   // the totals of the chunk before have been read
-    if (lane == 0) red[warp] = all[0] + all[1];
+    if (lane == 0) red[warp] = all;
     __syncthreads();
     const int t = red[lane];   // kPlanWarps == 32
-    int r = found + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? t : 0);
+    int at = found + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? t : 0) + before;
     found += __reduce_add_sync(0xFFFFFFFFu, t);
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      int at = r + before[k];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (mine[k] >> j & 1) {
-          if (at < want) list[at] = p0 + 128 * k + j;
-          ++at;
-        }
-      r += all[k];
-    }
+    for (int j = 0; j < 4; ++j)
+      if (mine >> j & 1) {
+        if (at < want) list[at] = static_cast<int>(p) + j;
+        ++at;
+      }
   }
   __syncthreads();
   return found;
@@ -199,7 +189,7 @@ __device__ __forceinline__ bool count_row(const mk_paged_cache& c, const Counts&
   bool bad = false;
   for_row(c.table + static_cast<long long>(s) * c.max_pages, first, last, [&](int, int p) {
     if (p >= 0 && p < c.n_pages)
-      atomicAdd(&ref.p[p], by);
+      ref.add(p, by);
     else
       bad = true;
   });
@@ -299,20 +289,18 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_resize(mk_paged_cache c,
       w.src[at] = was;
       w.dst[at] = page;
       w.rows[at] = low % ps;
-      atomicSub(&ref.p[was], 1);
-      ref.p[page] = 1;
+      ref.add(was, -1);
+      ref.take(page);
       row[e] = page;
     }
     for_row(take + mine - have, have, np, [&](int j, int p) {
       row[j] = p;
-      ref.p[p] = 1;
+      ref.take(p);
     });
     for (int j = np + lane; j < op; j += 32) row[j] = -1;
     __syncwarp();
     if (lane == 0) c.len[s] = lens ? lens[i] : 0;
   }
-  __syncthreads();
-  close_counts(c, ref);
 }
 
 // mk_pages_fork, the same phases: give back what the destinations hold, count the partly
@@ -387,13 +375,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_fork(mk_paged_cache c, c
     int* rb = c.table + static_cast<long long>(b) * c.max_pages;
     for_row(c.table + static_cast<long long>(a) * c.max_pages, 0, np, [&](int j, int p) {
       if (j < len / ps) {
-        atomicAdd(&ref.p[p], 1);
+        ref.add(p, 1);
       } else {
         const int page = list[need[i]], at = atomicAdd(&w.count[0], 1);
         w.src[at] = p;
         w.dst[at] = page;
         w.rows[at] = len % ps;
-        ref.p[page] = 1;
+        ref.take(page);
         p = page;
       }
       rb[j] = p;
@@ -402,8 +390,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_fork(mk_paged_cache c, c
     __syncwarp();
     if (lane == 0) c.len[b] = len;
   }
-  __syncthreads();
-  close_counts(c, ref);
 }
 
 // mk_pages_compact, counts and copies: pages in use, then the r-th used page with an id past
