@@ -23,7 +23,7 @@
 // softmax and epilogue. Values are taken as they lie in the page (transposed by the MMA descriptor).
 //
 // Measured on a B200, per call: one token of each of 64 sequences (1.27 GB of keys and values) 203 us, 95 % of the
-// measured copy bandwidth; a 4096-token prompt (8/2 heads of 256) 79 us, 870 TFLOP/s of causal work, where
+// measured copy bandwidth; a 4096-token prompt (8/2 heads of 256) 66 us, 1040 TFLOP/s of causal work, where
 // shared memory bounds a tile (128 x 128 tiles at 256 entries move 320 KB through it, 2560 clocks; measured 3400);
 // ragged chunks of 128-wide heads 70 us, bound by the chain of a group's softmax (about 3000 clocks a
 // tile, two groups at work); one token over 32769 positions 25 us, of which the stream of 67 MB is half.
@@ -85,6 +85,7 @@ struct AttnArgs {
   int over;                // key tiles that a full row tile's queries and results cost, beside one
   float c2;                // |scale| log2 e
   int negative;            // the sign of scale
+  int deal;                // row tiles may stay whole (at most 32 sequences then)
   NewRows w;
   float* part;             // [2 * grid][max_rows][D]
   float2* ml;              // [2 * grid][max_rows] (m, l)
@@ -306,7 +307,7 @@ __device__ __forceinline__ int key_tiles(const AttnArgs& a, const SeqWork& w, in
   const int keys = w.pos0 + min((j + 1) * a.tokens, w.rows);
   return max(1, (keys + kN - 1) / kN);
 }
-// What row tile j costs beside its key tiles, in units of them (a.over + 1 for 128 rows, 1 for a few). Measured, 256
+// What row tile j costs beside its key tiles, in units of them (a.over + 1 for 128 rows, 1 for a few). Measured, cut, 256
 // entries: a 4096-token prompt 79 us with 3 units, 81 with 2 and 80 with 4; 128 entries, ragged chunks: 68 us with 4, 69 with 3
 // and 5.
 __device__ __forceinline__ int extra_units(const AttnArgs& a, const SeqWork& w, int j) {
@@ -344,6 +345,83 @@ __device__ __forceinline__ long long warp_scan64(long long v) {   // inclusive
     if ((threadIdx.x & 31) >= o) v += y;
   }
   return v;
+}
+
+// Row tiles that stay whole. An even cut of the units costs each CTA about one more segment, two partial
+// results and their join; where the row tiles themselves fill the CTAs evenly enough it is left out: the
+// row tiles are put in the order of their key tiles and dealt to the CTAs there and back (CTA c takes ranks c,
+// 2 ctas - 1 - c, 2 ctas + c, ...). Nothing is sorted: the key tiles of a sequence's row tiles do not fall, so
+// how many of them have x or more is a formula, and a table of these sums finds the row tile of any rank.
+// Taken where the longest share is at most kSlack units above the even one. Measured over prompts of 1 to 12
+// sequences: with 2 to 5 units more 8 to 33 % faster (4096-token prompt, 8 heads of 256, 79 -> 66 us; three of 400
+// tokens, 16 heads, 31 -> 25), with 6 and 7 more 0 to 13 %, with 8 and 9 more the same, 9 % slower for heads of 64, with
+// 11 and more 3 to 17 % slower. Not looked at where it would cost more than it gives: row tiles of more than kMost
+// key tiles, more than kRounds of them a CTA (the cuts weigh little), more than 32 sequences, and sequences of
+// fewer than kM packed rows on average, whose partial results are small (decode of 32 sequences of 250
+// positions 14 us cut, 18 whole).
+constexpr int kMaxSeqs = 65536, kRounds = 8, kMost = 1024, kSlack = 7;
+struct Whole {
+  int4 seq[32][2];                               // pos0, rows, row tiles, row0; len, sequence
+  int load, limit, most, tiles, maybe;
+  Segment list[kRounds];
+  int count[kMost];                              // row tiles with more than i key tiles
+};
+// Row tiles of one kv head of a sequence with x key tiles or more: its last ones.
+__device__ __forceinline__ int tiles_from(int4 s, int tokens, int x) {
+  const int y = (x - 1) * kN - s.x;              // the first y rows see fewer
+  return x <= 1 || y < 0 ? s.z : y >= s.y ? 0 : s.z - y / tokens;
+}
+// Called by the whole CTA: its row tiles, in o->list, or -1 where the even cut is better. Not inlined: with its
+// code inside, ragged chunks that do not take it were 2 us of 70 slower.
+__device__ __noinline__ int plan_whole(const AttnArgs& a, Whole* o) {
+  const int ctas = gridDim.x, tiles = o->tiles, most = o->most;
+  for (int x = threadIdx.x; x < most; x += kThreads_) {
+    int count = 0;
+#pragma unroll 1
+    for (int i = 0; i < a.w.n; ++i) count += tiles_from(o->seq[i][0], a.tokens, x + 1);
+    o->count[x] = count * a.c.kv_heads;
+  }
+  __syncthreads();
+  auto rank_of = [&](int k, int c) { return k * ctas + (k & 1 ? ctas - 1 - c : c); };
+  auto size = [&](int rank) {                    // key tiles of the row tile of this rank
+    int lo = 1, hi = most;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (o->count[mid - 1] > rank) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  };
+  int load = 0;
+  for (int c = threadIdx.x; c < ctas; c += kThreads_) {
+    int mine = 0;
+#pragma unroll 1
+    for (int k = 0; k * ctas < tiles; ++k)
+      if (rank_of(k, c) < tiles) mine += size(rank_of(k, c)) + 1 + a.over;
+    load = max(load, mine);
+  }
+  load = __reduce_max_sync(0xFFFFFFFFu, load);
+  if ((threadIdx.x & 31) == 0) atomicMax(&o->load, load);
+  __syncthreads();
+  if (o->load > o->limit) return -1;
+  int n = 0;
+  const int k = static_cast<int>(threadIdx.x) - 10 * 32;   // the scheduler's lane, which reads the list
+  while (n < kRounds && rank_of(n, blockIdx.x) < tiles) ++n;
+  if (k >= 0 && k < n) {
+    const int rank = rank_of(k, blockIdx.x), x = size(rank);
+    int rel = rank - (x < most ? o->count[x] : 0);
+#pragma unroll 1
+    for (int i = 0; i < a.w.n; ++i) {
+      const int4 q = o->seq[i][0], r = o->seq[i][1];
+      const int above = tiles_from(q, a.tokens, x + 1), same = tiles_from(q, a.tokens, x) - above;
+      if (rel < same * a.c.kv_heads) {
+        o->list[k] = Segment{0, q.w, q.y, q.x, r.x, r.y, rel / same, q.z - above - 1 - rel % same, 0, x, -1};
+        break;
+      }
+      rel -= same * a.c.kv_heads;
+    }
+  }
+  return n;
 }
 
 template <int D>
@@ -405,20 +483,40 @@ __global__ void __launch_bounds__(kThreads_, 1)
   const int n_groups = (a.w.n + 31) / 32;
   SeqWork first{};           // the scheduler's warp keeps the first group
   long long first_units = 0;
+  constexpr int kGroupBytes = kMaxSeqs / 32 * sizeof(long long);
+  static_assert(kGroupBytes + sizeof(Whole) <= L::kSlots * L::kSlot, "fits the ring");
+  Whole* order = reinterpret_cast<Whole*>(ring + kGroupBytes);
   for (int g = (warp + kThreads_ / 32 - 10) % (kThreads_ / 32); g < n_groups; g += kThreads_ / 32) {
     int bad = 0;
     const SeqWork w = seq_work(a, g * 32 + lane, &bad);
     const long long hu = head_units(a, w), u = warp_sum64(hu) * a.c.kv_heads;
     if (lane == 0) groups[g] = u;
     if (g == 0) first = w, first_units = hu;
+    if (a.deal) {                                // one group
+      const int tiles = static_cast<int>(min(warp_sum64(w.row_tiles) * a.c.kv_heads, 1ll << 30));
+      const int mean = static_cast<int>(min(u, 1ll << 30)) / static_cast<int>(gridDim.x);
+      const int most = __reduce_max_sync(0xFFFFFFFFu, w.row_tiles > 0 ? key_tiles(a, w, w.row_tiles - 1) : 0);
+      order->seq[lane][0] = make_int4(w.pos0, w.rows, w.row_tiles, w.row0);
+      order->seq[lane][1] = make_int4(w.len, w.seq, 0, 0);
+      if (lane == 0) {
+        order->load = 0, order->most = most, order->tiles = tiles, order->limit = mean + kSlack;
+        order->maybe = tiles <= kRounds * static_cast<int>(gridDim.x) && most <= kMost &&
+                       most + 1 + a.over <= mean + kSlack;
+      }
+    }
     if (bad && blockIdx.x == 0) atomicOr(err, MK_DEVERR_BAD_PAGE);
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  int whole = -1;                                // row tiles of this CTA where all stay whole
+  if (a.deal && order->maybe) whole = plan_whole(a, order);
+  Segment planned{};                             // the scheduler's lane k: the k-th of them
   long long total = 0, before = 0, u0 = 0, u1 = 0;   // scheduler: all units, units before its group, its range
   int g = 0;
   if (warp == 10) {
+    __syncwarp();
+    if (lane < whole) planned = order->list[lane];
     for (int i = lane; i < n_groups; i += 32) total += groups[i];
     total = warp_sum64(total);
     const long long ctas = min(static_cast<long long>(gridDim.x), total);   // each with work, the first ones
@@ -465,55 +563,67 @@ __global__ void __launch_bounds__(kThreads_, 1)
     if (lane == 0) a.lead[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     __syncwarp();
     long long u = u0;
+    int taken = 0;
+    if (whole >= 0) u = 0, u1 = 1, g = 0;          // one pass over the only group
     for (; u < u1 && ok && g < n_groups; ++g) {
       int bad = 0;
       const SeqWork mine = g ? seq_work(a, g * 32 + lane, &bad) : first;
       const long long hu = g ? head_units(a, mine) : first_units, units = hu * a.c.kv_heads;
       const long long incl = before + warp_scan64(units);
       while (ok && u < u1) {
-        const unsigned past = __ballot_sync(0xFFFFFFFFu, incl > u);
-        if (!past) break;
-        const int src = __ffs(past) - 1;
-        const SeqWork w = shfl_work(mine, src);
-        const long long h = __shfl_sync(0xFFFFFFFFu, hu, src);
-        const long long rel = u - __shfl_sync(0xFFFFFFFFu, incl - units, src);
         Segment s{};
-        s.row0 = w.row0, s.new_rows = w.rows, s.pos0 = w.pos0, s.len = w.len, s.seq = w.seq;
-        s.kvh = static_cast<int>(rel / h);
-        long long rem = rel - s.kvh * h;           // units into this head
-        int tiles = 0;
-        for (int j0 = 0;; j0 += 32) {              // the row tile that holds unit rem of this head
-          const int t = j0 + lane < w.row_tiles ? extra_units(a, w, j0 + lane) + key_tiles(a, w, j0 + lane) : 0;
-          const long long inc = warp_scan64(t);
-          const unsigned hit = __ballot_sync(0xFFFFFFFFu, inc > rem);
-          if (hit) {
-            const int k = __ffs(hit) - 1;
-            s.tile = j0 + k;
-            tiles = __shfl_sync(0xFFFFFFFFu, t, k);
-            rem -= __shfl_sync(0xFFFFFFFFu, inc, k) - tiles;
-            break;
+        if (whole >= 0) {
+          if (taken == whole) break;
+          s.row0 = __shfl_sync(0xFFFFFFFFu, planned.row0, taken), s.new_rows = __shfl_sync(0xFFFFFFFFu, planned.new_rows, taken);
+          s.pos0 = __shfl_sync(0xFFFFFFFFu, planned.pos0, taken), s.len = __shfl_sync(0xFFFFFFFFu, planned.len, taken);
+          s.seq = __shfl_sync(0xFFFFFFFFu, planned.seq, taken), s.kvh = __shfl_sync(0xFFFFFFFFu, planned.kvh, taken);
+          s.tile = __shfl_sync(0xFFFFFFFFu, planned.tile, taken), s.t1 = __shfl_sync(0xFFFFFFFFu, planned.t1, taken);
+          s.part = -1;
+          ++taken;
+        } else {
+          const unsigned past = __ballot_sync(0xFFFFFFFFu, incl > u);
+          if (!past) break;
+          const int src = __ffs(past) - 1;
+          const SeqWork w = shfl_work(mine, src);
+          const long long h = __shfl_sync(0xFFFFFFFFu, hu, src);
+          const long long rel = u - __shfl_sync(0xFFFFFFFFu, incl - units, src);
+          s.row0 = w.row0, s.new_rows = w.rows, s.pos0 = w.pos0, s.len = w.len, s.seq = w.seq;
+          s.kvh = static_cast<int>(rel / h);
+          long long rem = rel - s.kvh * h;           // units into this head
+          int tiles = 0;
+          for (int j0 = 0;; j0 += 32) {              // the row tile that holds unit rem of this head
+            const int t = j0 + lane < w.row_tiles ? extra_units(a, w, j0 + lane) + key_tiles(a, w, j0 + lane) : 0;
+            const long long inc = warp_scan64(t);
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, inc > rem);
+            if (hit) {
+              const int k = __ffs(hit) - 1;
+              s.tile = j0 + k;
+              tiles = __shfl_sync(0xFFFFFFFFu, t, k);
+              rem -= __shfl_sync(0xFFFFFFFFu, inc, k) - tiles;
+              break;
+            }
+            rem -= __shfl_sync(0xFFFFFFFFu, inc, 31);
           }
-          rem -= __shfl_sync(0xFFFFFFFFu, inc, 31);
-        }
-        // tiles counts the extra units and then the key tiles; a run that ends in the former leaves the
-        // row tile to the next CTA
-        const int over = extra_units(a, w, s.tile);
-        const int upto = static_cast<int>(min(static_cast<long long>(tiles), rem + (u1 - u)));
-        u += upto - rem;
-        s.t0 = max(0, static_cast<int>(rem) - over);
-        s.t1 = upto - over;
-        if (s.t1 <= s.t0) continue;
-        tiles -= over;
-        const bool whole = s.t0 == 0 && s.t1 == tiles;
-        s.part = whole ? -1 : static_cast<int>(blockIdx.x) * 2 + (made ? 1 : 0);
-        ++made;
-        if (!whole && s.t0 == 0 && lane == 0) {
-          // the CTA whose run holds the row tile's last unit: the largest c with total c / ctas <= that unit
-          const long long end = u + (tiles - s.t1), ctas = min(static_cast<long long>(gridDim.x), total);
-          const int last = static_cast<int>((end * ctas + total - 1) / total) - 1;
-          a.lead[2 * blockIdx.x] = make_int4(s.part, last - static_cast<int>(blockIdx.x) + 1,
-                                             min(a.tokens, w.rows - s.tile * a.tokens) * a.group, s.tile);
-          a.lead[2 * blockIdx.x + 1] = make_int4(s.kvh, s.row0, 0, 0);
+          // tiles counts the extra units and then the key tiles; a run that ends in the former leaves the
+          // row tile to the next CTA
+          const int over = extra_units(a, w, s.tile);
+          const int upto = static_cast<int>(min(static_cast<long long>(tiles), rem + (u1 - u)));
+          u += upto - rem;
+          s.t0 = max(0, static_cast<int>(rem) - over);
+          s.t1 = upto - over;
+          if (s.t1 <= s.t0) continue;
+          tiles -= over;
+          const bool whole = s.t0 == 0 && s.t1 == tiles;
+          s.part = whole ? -1 : static_cast<int>(blockIdx.x) * 2 + (made ? 1 : 0);
+          ++made;
+          if (!whole && s.t0 == 0 && lane == 0) {
+            // the CTA whose run holds the row tile's last unit: the largest c with total c / ctas <= that unit
+            const long long end = u + (tiles - s.t1), ctas = min(static_cast<long long>(gridDim.x), total);
+            const int last = static_cast<int>((end * ctas + total - 1) / total) - 1;
+            a.lead[2 * blockIdx.x] = make_int4(s.part, last - static_cast<int>(blockIdx.x) + 1,
+                                               min(a.tokens, w.rows - s.tile * a.tokens) * a.group, s.tile);
+            a.lead[2 * blockIdx.x + 1] = make_int4(s.kvh, s.row0, 0, 0);
+          }
         }
         emit(s);
       }
@@ -1054,7 +1164,7 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
   using mk::refuse;
   if (const char* why = mk::paged_cache_problem(c)) return refuse(why);
   if (layer < 0 || layer >= c->n_layers) return refuse("layer out of range");
-  if (rows < 0 || n < 0 || n > 65536) return refuse("rows must not be negative, n must lie in 0 .. 65536");
+  if (rows < 0 || n < 0 || n > mk::kMaxSeqs) return refuse("rows must not be negative, n must lie in 0 .. 65536");
   if (q_heads < 1 || q_heads % c->kv_heads) return refuse("q_heads must be a positive multiple of kv_heads");
   if (!(scale > -INFINITY && scale < INFINITY)) return refuse("scale must be finite");
   if (q_heads / c->kv_heads > mk::kM) return refuse("at most 128 query heads per kv head");
@@ -1080,6 +1190,7 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
     const mk::AttnArgs a{*c, layer, rows, q_heads, q_heads / c->kv_heads, box, static_cast<const uint16_t*>(d_q), ldq,
                          static_cast<uint16_t*>(d_out), ldo, mk::kM / (q_heads / c->kv_heads),
                          std::min(mk::kM / (q_heads / c->kv_heads), (rows + n - 1) / n), c->head_dim == 256 ? 2 : c->head_dim == 128 ? 3 : 5, c2, scale < 0 ? 1 : 0,
+                         n <= 32 && static_cast<int64_t>(rows) * (q_heads / c->kv_heads) >= static_cast<int64_t>(n) * mk::kM ? 1 : 0,
                          mk::NewRows{d_seq_start, d_seqs, n}, reinterpret_cast<float*>(ws), reinterpret_cast<float2*>(ws + sc.ml),
                          reinterpret_cast<int4*>(ws + sc.lead), max_rows};
     CUtensorMap tq, tq1, tk, tv;

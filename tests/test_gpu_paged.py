@@ -215,6 +215,16 @@ def test_attention_prompt(d, hq, hkv):
     run_attention(d, [700, 1500], [333, 1], hq, hkv, d, 16, layer=1, layers=3, pad=3)
 
 
+# prompts whose row tiles stay whole (one to seven for each of 148 CTAs), that are cut, and that are either way
+# beside sequences without rows, without positions and with rows before the first position
+@pytest.mark.parametrize("hq,hkv,d,lens,new", [(32, 4, 64, [900, 2100, 1500], [900, 2000, 700]), (8, 2, 256, [2600], [2600]),
+                                               (16, 4, 128, [1900, 0, 1300, 40], [1700, 3, 0, 700]), (12, 2, 256, [70, 9000], [70, 400]),
+                                               (64, 8, 64, [1700] * 2, [1650] * 2), (3, 1, 128, [1030] * 31 + [1], [128] * 31 + [1]),
+                                               (128, 1, 64, [140, 1200], [140, 300]), (4, 4, 128, [513, 1, 2000], [300, 1, 1999])])
+def test_attention_of_whole_row_tiles(hq, hkv, d, lens, new):
+    run_attention(71, lens, new, hq, hkv, d, 16)
+
+
 @pytest.mark.parametrize("d", [64, 256])
 def test_attention_large_scores_and_scales(d):
     """Scores spanning hundreds of units, in both signs of the scale, and a scale of zero (the mean)."""
