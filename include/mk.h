@@ -428,7 +428,8 @@ int mk_qk_norm_rope(const mk_qk_rope* a, void* stream);
  * (negative position) gives zeros; rows outside [seq_start[0], seq_start[n]) are left as they
  * are. Keys and values below a sequence's length must be finite; what lies past it, in its
  * last page or in pages the table does not name, is never part of a result. A page id out of range sets
- * MK_DEVERR_BAD_PAGE and reads as zeros.
+ * MK_DEVERR_BAD_PAGE and reads as zeros. The kernel's waits are bounded: one that gave up sets
+ * MK_DEVERR_PIPE_TIMEOUT, and the call's results are then not valid.
  * d_q: bf16 [rows][q_heads][head_dim], d_out: bf16 likewise, ldq / ldo elements from row to
  * row (multiples of 8); 16-byte aligned. n <= 65536. q_heads a multiple of the cache's kv_heads, at most 128 times them.
  * d_scratch: at least mk_paged_attention_scratch(...) bytes, 32-byte aligned; one buffer per
