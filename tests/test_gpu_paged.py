@@ -646,6 +646,36 @@ def test_captured_calls_follow_lengths_and_tables():
             assert np.all(np.abs(f64(go[i:i + 1]) - want) <= ref.attention_bound(want, mag, big, 128 ** -0.5, 128))
 
 
+def test_captured_prompts_whole_and_cut():
+    """One captured call replayed on lengths whose row tiles stay whole, are cut, and stay whole again."""
+    torch.manual_seed(4)
+    c = hda().PagedCache.empty(1, 500, 2, 16, 64, 2, 400)
+    rows = 700
+    seqs, lens, start = ints([1, 0]), ints([350, 350]), ints([0, 350, rows])
+    q = torch.randn(rows, 8, 64, device="cuda").bfloat16()
+    c.k.normal_()
+    c.v.normal_()
+    c.resize(seqs, lens)
+    c.attention(0, q, start, seqs)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.resize(seqs, lens)
+        out = c.attention(0, q, start, seqs)
+    for a, b, cut in ((400, 360, 350), (2, 6300, 2), (1200, 330, 300)):
+        lens.copy_(ints([a, b]))
+        start.copy_(ints([0, cut, rows]))
+        out.fill_(7.0)
+        g.replay()
+        assert int(c.err.item()) == 0
+        for s, n, lo, hi in ((1, a, 0, cut), (0, b, cut, rows)):
+            row = c.table[s].cpu().numpy()
+            k, v = gather(c.k, 0, row, n, 16), gather(c.v, 0, row, n, 16)
+            pos = np.arange(n - (hi - lo), n)
+            want, mag, big = ref.attention(f64(q[lo:hi]), k, v, pos, 64 ** -0.5)
+            assert np.all(np.abs(f64(out[lo:hi]) - want) <= ref.attention_bound(want, mag, big, 64 ** -0.5, 64))
+            assert (out[lo:hi][torch.from_numpy(pos < 0).cuda()] == 0).all()
+
+
 def test_captured_page_calls():
     """Fork, resize and compaction captured once and replayed on changed lists."""
     c = hda().PagedCache.empty(2, 60, 2, 8, 64, 6, 8)
