@@ -1,0 +1,47 @@
+"""Order inside and between paged-cache calls: roles of the attention kernel that run late, streams, devices and threads."""
+import ctypes as C
+import os
+import subprocess
+
+import pytest
+
+import test_gpu_paged as base
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def late_reader(tmp_path_factory):
+    """mk_paged_attention of a build in which one softmax group waits 20 us before it reads a row tile's results."""
+    from hybrid_deltanet_attention_b200 import _abi, build
+    d = tmp_path_factory.mktemp("late_reader")
+    obj, so = str(d / "paged_attn.o"), str(d / "libmk_late.so")
+    flags = [f for f in build.FLAGS if f != "-shared"]
+    src = os.path.join(build.CSRC, "paged_attn.cu")
+    subprocess.check_call([build.nvcc(), *build.ARCH, *flags, "-DMK_TEST_SLOW_EPILOGUE_NS=20000", "-c", src, "-o", obj])
+    subprocess.check_call([build.nvcc(), *build.ARCH, "-shared", "-Xcompiler", "-fPIC", obj, build.LIB, "-o", so])
+    fn = C.CDLL(so).mk_paged_attention
+    own = _abi.load_library().mk_paged_attention
+    fn.argtypes, fn.restype = own.argtypes, own.restype
+    assert C.cast(fn, C.c_void_p).value != C.cast(own, C.c_void_p).value
+    return fn
+
+
+# CTAs with several row tiles: cut ones with partial results, whole ones, and both kinds beside empty sequences
+@pytest.mark.parametrize("hq,hkv,d,lens,new", [(8, 2, 256, [2600], [2600]), (8, 2, 256, [70, 9000, 0, 300], [70, 400, 2, 300]),
+                                               (16, 4, 128, [1900, 1300, 40], [1700, 3, 40]), (16, 4, 128, [200] * 150, [3] * 150),
+                                               (32, 4, 64, [900, 2100, 1500], [900, 2000, 700]), (12, 2, 64, [500, 77] * 60, [1] * 120)])
+def test_a_row_tile_read_late_keeps_its_results(late_reader, monkeypatch, hq, hkv, d, lens, new):
+    """The next row tile's first product must not overwrite O while a softmax group still reads the one before."""
+    want, _ = base.run_attention(31, lens, new, hq, hkv, d, 16)
+    cls = base.hda().PagedCache
+    init = cls.__init__
+
+    def late(self, *a, **kw):
+        init(self, *a, **kw)
+        self._attention = late_reader
+
+    monkeypatch.setattr(cls, "__init__", late)
+    got, c = base.run_attention(31, lens, new, hq, hkv, d, 16)   # against float64 too
+    assert c._attention is late_reader and torch.equal(got, want)
