@@ -110,7 +110,7 @@ struct Segment {
 };
 
 struct Bars {
-  uint64_t full[8], empty[8], s_full[3], p_full[3], o_done[2], q_full, q_free, pair[4], m_full[2][4], seg_full[kSegs], seg_empty[kSegs];
+  uint64_t full[8], empty[8], s_full[3], p_full[3], o_done[2], mma_end, q_full, q_free, pair[4], m_full[2][4], seg_full[kSegs], seg_empty[kSegs];
   uint32_t tmem;
   int abort;
   Segment seg[kSegs];
@@ -459,6 +459,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
       mbar_init(&b->m_full[0][i], 1);
       mbar_init(&b->m_full[1][i], 1);
     }
+    mbar_init(&b->mma_end, 1);
     mbar_init(&b->q_full, 1);
     mbar_init(&b->q_free, 1);
     for (int i = 0; i < kSegs; ++i) {
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
     uint32_t base = 0, last = 0;                   // ring slots before the segment; the last one filled, plus one
     bool ok = true;
     for (int i = 0; ok; ++i) {
-      if (!warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) break;
+      if (!(ok = warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err))) break;
       const Segment s = b->seg[i % kSegs];
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->seg_empty[i % kSegs]);
@@ -743,7 +744,7 @@ __global__ void __launch_bounds__(kThreads_, 1)
       sbuf = sbuf == L::kBufs - 1 ? 0 : sbuf + 1;
     };
     for (int i = 0; ok; ++i) {
-      if (!warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err)) break;
+      if (!(ok = warp_wait(b, &b->seg_full[i % kSegs], (i / kSegs) & 1, err))) break;
       const int len = b->seg[i % kSegs].len, n = b->seg[i % kSegs].t1 - b->seg[i % kSegs].t0, end = b->seg[i % kSegs].end;
       __syncwarp();
       if (lane == 0) mbar_arrive(&b->seg_empty[i % kSegs]);
@@ -772,6 +773,11 @@ __global__ void __launch_bounds__(kThreads_, 1)
         if (ok) commit(&b->o_done[it & 1], issue);
         ++it;
       }
+    }
+    if (!ok) {                                     // products in flight end before TMEM is given back (bounded)
+      int never = 0;
+      commit(&b->mma_end, issue);
+      if (lane == 0) mbar_wait(&b->mma_end, 0, &never, kWaitNs / 10);
     }
     __syncwarp();
   }

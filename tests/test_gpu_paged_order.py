@@ -3,6 +3,7 @@ import ctypes as C
 import os
 import subprocess
 
+import numpy as np
 import pytest
 
 import test_gpu_paged as base
@@ -11,21 +12,24 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 
-@pytest.fixture(scope="module")
-def late_reader(tmp_path_factory):
-    """mk_paged_attention of a build in which one softmax group waits 20 us before it reads a row tile's results."""
+def late_build(d, ns):
+    """mk_paged_attention of a build in which one softmax group waits `ns` before it reads a row tile's results."""
     from hybrid_deltanet_attention_b200 import _abi, build
-    d = tmp_path_factory.mktemp("late_reader")
-    obj, so = str(d / "paged_attn.o"), str(d / "libmk_late.so")
+    obj, so = str(d / "paged_attn.o"), str(d / f"libmk_late_{ns}.so")
     flags = [f for f in build.FLAGS if f != "-shared"]
     src = os.path.join(build.CSRC, "paged_attn.cu")
-    subprocess.check_call([build.nvcc(), *build.ARCH, *flags, "-DMK_TEST_SLOW_EPILOGUE_NS=20000", "-c", src, "-o", obj])
+    subprocess.check_call([build.nvcc(), *build.ARCH, *flags, f"-DMK_TEST_SLOW_EPILOGUE_NS={ns}ull", "-c", src, "-o", obj])
     subprocess.check_call([build.nvcc(), *build.ARCH, "-shared", "-Xcompiler", "-fPIC", obj, build.LIB, "-o", so])
     fn = C.CDLL(so).mk_paged_attention
     own = _abi.load_library().mk_paged_attention
     fn.argtypes, fn.restype = own.argtypes, own.restype
     assert C.cast(fn, C.c_void_p).value != C.cast(own, C.c_void_p).value
     return fn
+
+
+@pytest.fixture(scope="module")
+def late_reader(tmp_path_factory):
+    return late_build(tmp_path_factory.mktemp("late_reader"), 20000)
 
 
 # CTAs with several row tiles: cut ones with partial results, whole ones, and both kinds beside empty sequences
@@ -45,3 +49,22 @@ def test_a_row_tile_read_late_keeps_its_results(late_reader, monkeypatch, hq, hk
     monkeypatch.setattr(cls, "__init__", late)
     got, c = base.run_attention(31, lens, new, hq, hkv, d, 16)   # against float64 too
     assert c._attention is late_reader and torch.equal(got, want)
+
+
+def test_a_wait_that_gives_up_ends_the_call_with_an_error(tmp_path):
+    """A group that reads 1.3 s late outlasts the kernel's waits of one second: every role gives up, what is in flight ends,
+    the call reports it, and the next call is right again."""
+    m = base.hda()
+    rng = np.random.default_rng(1)
+    c, table = base.make_cache(rng, [2600], 16, 2, 128)
+    q, start = torch.randn(2600, 8, 128, device="cuda").bfloat16(), base.ints([0, 2600])
+    want, own = c.attention(0, q, start), c._attention
+    c.sync()
+    c._attention = late_build(tmp_path, 1300000000)
+    c.attention(0, q, start)
+    with pytest.raises(m.MkError, match="gave up"):
+        c.sync()
+    c._attention = own
+    got = c.attention(0, q, start)
+    c.sync()
+    assert torch.equal(got, want)
