@@ -31,6 +31,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cuda.h>
+#include <limits>
 #include <string>
 
 #include "dev.cuh"
@@ -1182,7 +1183,7 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
   if (layer < 0 || layer >= c->n_layers) return refuse("layer out of range");
   if (rows < 0 || n < 0 || n > mk::kMaxSeqs) return refuse("rows must not be negative, n must lie in 0 .. 65536");
   if (q_heads < 1 || q_heads % c->kv_heads) return refuse("q_heads must be a positive multiple of kv_heads");
-  if (!(scale > -INFINITY && scale < INFINITY)) return refuse("scale must be finite");
+  if (!(std::fabs(scale) <= 2e38f)) return refuse("scale must lie within -2e38 .. 2e38");   // its log2 units are an fp32 factor
   if (q_heads / c->kv_heads > mk::kM) return refuse("at most 128 query heads per kv head");
   if (rows == 0 || n == 0) return MK_OK;
   const int64_t dq = static_cast<int64_t>(q_heads) * c->head_dim;
@@ -1200,9 +1201,9 @@ extern "C" int mk_paged_attention(const mk_paged_cache* c, int32_t layer, const 
     if (scratch_bytes < sc.total) return refuse("scratch too small");
     uint8_t* ws = static_cast<uint8_t*>(d_scratch);
     const int box = std::min(128, c->page_size & -c->page_size);
-    // a scale of zero (the mean of the values) keeps a factor that is lost beside any score, so that a
-    // masked score stays minus infinity
-    const float c2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1e-30f);
+    // A scale of zero (the mean of the values) becomes the smallest factor there is, so that a masked score stays
+    // minus infinity: times any fp32 score it is below 2^-20.
+    const float c2 = std::max(std::fabs(scale) * 1.4426950408889634f, std::numeric_limits<float>::denorm_min());
     const mk::AttnArgs a{*c, layer, rows, q_heads, q_heads / c->kv_heads, box, static_cast<const uint16_t*>(d_q), ldq,
                          static_cast<uint16_t*>(d_out), ldo, mk::kM / (q_heads / c->kv_heads),
                          std::min(mk::kM / (q_heads / c->kv_heads), (rows + n - 1) / n), c->head_dim == 256 ? 2 : c->head_dim == 128 ? 3 : 5, c2, scale < 0 ? 1 : 0,

@@ -430,6 +430,7 @@ int mk_qk_norm_rope(const mk_qk_rope* a, void* stream);
  * last page or in pages the table does not name, is never part of a result. A page id out of range sets
  * MK_DEVERR_BAD_PAGE and reads as zeros. The kernel's waits are bounded: one that gave up sets
  * MK_DEVERR_PIPE_TIMEOUT, and the call's results are then not valid.
+ * scale: any value of magnitude at most 2e38, 0 and negative ones too; scaled scores must stay in fp32's range.
  * d_q: bf16 [rows][q_heads][head_dim], d_out: bf16 likewise, ldq / ldo elements from row to
  * row (multiples of 8); 16-byte aligned. n <= 65536. q_heads a multiple of the cache's kv_heads, at most 128 times them.
  * d_scratch: at least mk_paged_attention_scratch(...) bytes, 32-byte aligned; one buffer per
