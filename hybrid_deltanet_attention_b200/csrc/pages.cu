@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_fork(mk_paged_cache c, c
 
 // mk_pages_compact, counts and copies: pages in use, then the r-th used page with an id past
 // them paired with the r-th free id below (there are equally many). list[p] is the new id of
-// a moved page p; the table follows in the copy kernel. Four counts a thread and step.
+// page p >= live, -1 where it has no count; the table follows in the copy kernel. Four counts a thread and step.
 __global__ void __launch_bounds__(kPlanThreads, 1) plan_compact(mk_paged_cache c) {
   __shared__ int red[32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_compact(mk_paged_cache c
       if (p + k >= c.n_pages) continue;
       hole |= (p + k < live && r[k] <= 0) << k;
       mover |= (p + k >= live && r[k] > 0) << k;
+      if (p + k >= live && r[k] <= 0) w.list[p + k] = -1;   // (what an earlier call left there is not this one's)
     }
     int total;   // both counts in one scan: holes in the low half, movers in the high half
     const int s = block_scan(static_cast<int>(__popc(hole) | __popc(mover) << 16), &total, red);
@@ -465,9 +466,8 @@ __device__ void remap_table(const mk_paged_cache& c) {
   for (unsigned i = blockIdx.x * blockDim.x + threadIdx.x; i < total; i += gridDim.x * blockDim.x) {
     const int s = i / c.max_pages, j = i - s * c.max_pages, p = c.table[i];
     if (static_cast<long long>(j) * c.page_size >= c.len[s] || p < live || p >= c.n_pages) continue;
-    // a page that is named but not counted in ref stays where it is
     const int to = w.list[p];
-    if (to >= 0 && to < live) c.table[i] = to;
+    if (to >= 0) c.table[i] = to;   // a page that is named but not counted in ref stays where it is
   }
 }
 
