@@ -104,6 +104,7 @@ class PagedCache:
     are contiguous (the same for both). table: int32 [sequences][max pages], -1 where a
     sequence has no page. len: int32 [sequences]. ref: int32 [pages], table entries per page.
     All stay the caller's tensors and are updated in place, on the device, in stream order.
+    A captured call uses the cache's own arrays too: keep the cache as long as its graphs.
     """
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, len: torch.Tensor, ref: torch.Tensor,
@@ -140,6 +141,10 @@ class PagedCache:
         self._scratch, self._scratch_for = 0, None
         self._attention = self.lib.mk_paged_attention
         self._bytes = torch.empty(0, dtype=torch.uint8, device=k.device)
+        # err and work are made on the stream that is current now; the others wait for that (see _first_use)
+        self._streams = set()
+        with torch.cuda.device(k.device):
+            self._made = None if torch.cuda.is_current_stream_capturing() else torch.cuda.current_stream().record_event()
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, kv_heads: int, page_size: int, head_dim: int, n_seqs: int, max_pages: int,
@@ -150,6 +155,28 @@ class PagedCache:
         return cls(k, v, torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=dev),
                    torch.zeros(n_seqs, dtype=torch.int32, device=dev), torch.zeros(n_pages, dtype=torch.int32, device=dev))
 
+    # ---- streams ----
+    def _first_use(self, stream: Optional[torch.cuda.Stream]) -> None:
+        """Where the stream of a call has not worked on this cache yet: it waits until the cache's own arrays are made,
+        and none of its memory is given to anything else before that stream has run, should the cache be dropped after a call."""
+        if (_raw_stream(self._index) if stream is None else stream.cuda_stream) in self._streams:
+            return
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        _need(stream.device == self.device, f"the stream is on {stream.device}, the tensors on {self.device}")
+        with torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if not capturing:                        # (a capture cannot wait for what it does not hold)
+            self._streams.add(stream.cuda_stream)
+            if self._made is not None:
+                stream.wait_event(self._made)
+        for t in (self.k, self.v, self.table, self.len, self.ref, self.work, self.err):
+            t.record_stream(stream)
+
+    def _on(self, stream: Optional[torch.cuda.Stream]):
+        self._first_use(stream)
+        return _on(self.device, stream)
+
     # ---- pages ----
     def _movable(self) -> None:
         _need(not self.fixed, "the pages of this cache belong to a model and keep their places")
@@ -159,7 +186,7 @@ class PagedCache:
         self._movable()
         s, l = _ints(seqs, "seqs", self._index), _ints(lens, "lens", self._index)   # noqa: E741
         _need(seqs.numel() == lens.numel(), "seqs and lens differ in length")
-        with _on(self.device, stream) as st:
+        with self._on(stream) as st:
             check(self.lib.mk_pages_resize(self._p, s, l, seqs.numel(), st))
         _used_on(stream, seqs, lens)
 
@@ -167,7 +194,7 @@ class PagedCache:
         """Give back every page of these sequences."""
         self._movable()
         s = _ints(seqs, "seqs", self._index)
-        with _on(self.device, stream) as st:
+        with self._on(stream) as st:
             check(self.lib.mk_pages_resize(self._p, s, None, seqs.numel(), st))
         _used_on(stream, seqs)
 
@@ -176,14 +203,14 @@ class PagedCache:
         self._movable()
         a, b = _ints(src, "src", self._index), _ints(dst, "dst", self._index)
         _need(src.numel() == dst.numel(), "src and dst differ in length")
-        with _on(self.device, stream) as st:
+        with self._on(stream) as st:
             check(self.lib.mk_pages_fork(self._p, a, b, src.numel(), st))
         _used_on(stream, src, dst)
 
     def compact(self, stream=None) -> None:
         """Move the used pages to the lowest ids (mk_pages_compact)."""
         self._movable()
-        with _on(self.device, stream) as st:
+        with self._on(stream) as st:
             check(self.lib.mk_pages_compact(self._p, st))
 
     def copy_pages(self, src: torch.Tensor, dst: torch.Tensor, source: Optional["PagedCache"] = None, stream=None) -> None:
@@ -192,7 +219,8 @@ class PagedCache:
         _need(f.device == self.device, "the caches are on different devices")
         a, b = _ints(src, "src", self._index), _ints(dst, "dst", self._index)
         _need(src.numel() == dst.numel(), "src and dst differ in length")
-        with _on(self.device, stream) as st:
+        f._first_use(stream)
+        with self._on(stream) as st:
             check(self.lib.mk_pages_copy(f._p, self._p, a, b, src.numel(), st))
         _used_on(stream, src, dst)
 
@@ -222,7 +250,7 @@ class PagedCache:
         if self._scratch_for != (rows, hq):          # bytes for calls of this shape
             self._scratch = max(32, self.lib.mk_paged_attention_scratch(self._p, rows, hq))
             self._scratch_for = (rows, hq)
-        with _on(self.device, stream) as st:
+        with self._on(stream) as st:
             if out is None:
                 out = torch.empty_like(q)
                 op = out.data_ptr()
@@ -237,10 +265,11 @@ class PagedCache:
 
     def sync(self, stream=None) -> None:
         """Wait for the stream and raise if a call found bad ids, lengths or too few pages (the word is then cleared)."""
-        (stream if stream is not None else torch.cuda.current_stream(self.device)).synchronize()
-        bits = int(self.err.item())
+        with self._on(stream):                    # read and cleared there: in order with the calls on that stream
+            bits = int(self.err.item())
+            if bits:
+                self.err.zero_()
         if bits:
-            self.err.zero_()
             names = [n for b, n in ((_abi.MK_DEVERR_BAD_PAGE, "a sequence, page, length or position out of range, or an id given twice"),
                                     (_abi.MK_DEVERR_NO_PAGES, "not enough free pages"),
                                     (_abi.MK_DEVERR_PIPE_TIMEOUT, "a pipeline wait gave up")) if bits & b]
@@ -284,7 +313,7 @@ def _rope(dev, q, k, v, positions, q_gain, k_gain, eps, theta, rot_dim, q_out, k
     gq = 0 if q_gain is None else _gain(q_gain, index, d)
     gk = 0 if k_gain is None else _gain(k_gain, index, d)
 
-    with _on(dev, stream) as st:
+    with (_on(dev, stream) if cache is None else cache._on(stream)) as st:
         # a fresh output is contiguous: the heads of a row are, and rows that are further apart are packed
         if q_out is None:
             q_out = torch.empty_like(q, dtype=_BF16)

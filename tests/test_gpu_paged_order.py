@@ -68,3 +68,78 @@ def test_a_wait_that_gives_up_ends_the_call_with_an_error(tmp_path):
     got = c.attention(0, q, start)
     c.sync()
     assert torch.equal(got, want)
+
+
+# ------------------------------------------------------------------ streams
+BUSY = 200_000_000                                 # clocks that a stream is kept busy, about 0.1 s
+
+
+def test_a_cache_dropped_after_a_call_on_a_given_stream():
+    """Its table and its own arrays are not given to anything else while the call still waits on that stream."""
+    m = base.hda()
+    torch.manual_seed(0)
+    c, table = base.make_cache(np.random.default_rng(0), [900, 700], 16, 2, 64)
+    q, start, s = torch.randn(60, 4, 64, device="cuda").bfloat16(), base.ints([0, 20, 60]), torch.cuda.Stream()
+    want = c.attention(0, q, start)
+    c.sync()
+    other = torch.flip(c.table, (0,)).contiguous()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+    got = m.PagedCache(c.k, c.v, c.table.clone(), c.len.clone(), c.ref.clone()).attention(0, q, start, stream=s)
+    keep = [torch.full_like(c.len, 3) for _ in range(64)] + [other.clone() for _ in range(64)] + [torch.ones_like(c.err) for _ in range(64)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(keep) == 192
+
+
+def test_a_source_cache_dropped_after_a_copy_on_a_given_stream():
+    m = base.hda()
+    to, s = m.PagedCache.empty(1, 4, 2, 16, 64, 1, 1), torch.cuda.Stream()
+    fr = m.PagedCache.empty(1, 4, 2, 16, 64, 1, 1)
+    fr.k.normal_()
+    fr.v.normal_()
+    k, v, ids = fr.k.clone(), fr.v.clone(), base.ints(range(4))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(BUSY)
+    to.copy_pages(ids, ids, source=fr, stream=s)
+    del fr
+    keep = [torch.zeros_like(k) for _ in range(64)]
+    torch.cuda.synchronize()
+    assert torch.equal(to.k, k) and torch.equal(to.v, v) and len(keep) == 64
+
+
+def test_the_error_word_is_in_order_with_the_calls_of_a_stream():
+    """It is cleared before the first call on any stream, and sync(stream) reads and clears it between that stream's calls."""
+    m = base.hda()
+    s, seqs, lens = torch.cuda.Stream(), base.ints([9]), base.ints([1])       # a sequence that does not exist
+    t = m.PagedCache.empty(1, 4, 1, 8, 64, 2, 2)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)                        # the current stream is busy: a new cache's arrays are cleared after that
+    c = m.PagedCache(t.k, t.v, t.table, t.len, t.ref)
+    c.resize(seqs, lens, stream=s)
+    with pytest.raises(m.MkError):
+        c.sync(s)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    c.resize(seqs, lens, stream=s)
+    with pytest.raises(m.MkError):
+        c.sync(s)
+    c.resize(seqs, lens, stream=s)                 # a second error, while the current stream is still busy
+    torch.cuda.synchronize()
+    with pytest.raises(m.MkError):
+        c.sync(s)
+    c.sync(s)
+    c.sync()
+
+
+def test_a_call_on_a_stream_of_another_device_is_refused():
+    m = base.hda()
+    c = m.PagedCache.empty(1, 4, 1, 8, 64, 2, 2)
+
+    class Elsewhere:
+        device, cuda_stream = torch.device("cuda", 7), 12345
+
+    for call in (lambda: c.compact(stream=Elsewhere()), lambda: c.sync(Elsewhere())):
+        with pytest.raises(ValueError, match="the stream is on"):
+            call()
