@@ -138,7 +138,7 @@ class PagedCache:
         self._p, self._address = C.byref(c), C.addressof(c)
         self._d, self._kv_heads, self._n_seqs = c.head_dim, c.kv_heads, c.n_seqs
         self._scale = 1.0 / math.sqrt(c.head_dim)
-        self._scratch, self._scratch_for = 0, None
+        self._scratch = (0, 0, 0)                # rows, query heads and the bytes for calls of this shape, replaced in one piece
         self._attention = self.lib.mk_paged_attention
         self._bytes = torch.empty(0, dtype=torch.uint8, device=k.device)
         # err and work are made on the stream that is current now; the others wait for that (see _first_use)
@@ -247,14 +247,14 @@ class PagedCache:
             _need(ho == hq, "out must have q's shape")
         else:
             op, ldo = 0, hq * d
-        if self._scratch_for != (rows, hq):          # bytes for calls of this shape
-            self._scratch = max(32, self.lib.mk_paged_attention_scratch(self._p, rows, hq))
-            self._scratch_for = (rows, hq)
         with self._on(stream) as st:
+            for_rows, for_heads, size = self._scratch
+            if for_rows != rows or for_heads != hq:  # asked with the tensors' device current: it goes by that GPU
+                size = max(32, self.lib.mk_paged_attention_scratch(self._p, rows, hq))
+                self._scratch = rows, hq, size
             if out is None:
                 out = torch.empty_like(q)
                 op = out.data_ptr()
-            size = self._scratch
             scratch = self._bytes.new_empty(size)
             rc = self._attention(self._p, layer, qp, ldq, rows, hq, start, ids, n, self._scale if scale is None else scale, op, ldo,
                                  scratch.data_ptr(), size, st)
