@@ -228,7 +228,7 @@ extern "C" int mk_qk_norm_rope(const mk_qk_rope* a, void* stream) {
   if (a->rows < 0 || a->q_heads < 1 || a->kv_heads < 1) return refuse("bad row or head count");
   if (a->rot_dim < 0 || a->rot_dim > a->head_dim || a->rot_dim % (a->head_dim / 16))
     return refuse("rot_dim must be a multiple of head_dim / 16, at most head_dim");
-  if (!(a->theta > 0) || !(a->eps >= 0)) return refuse("theta must be positive and eps not negative");
+  if (!(a->theta > 0) || std::isinf(a->theta) || !(a->eps >= 0)) return refuse("theta must be positive and finite, eps not negative");
   const mk_paged_cache* c = a->cache;
   if (c) {
     if (const char* why = mk::paged_cache_problem(c)) return refuse(why);

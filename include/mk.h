@@ -402,7 +402,7 @@ typedef struct mk_qk_rope {
   int32_t  dtype;               /* of q, k, v: MK_DT_F32 or MK_DT_BF16 */
   int32_t  rows, q_heads, kv_heads, head_dim;   /* head_dim 64, 128 or 256 */
   int32_t  rot_dim;             /* 0 .. head_dim, a multiple of head_dim/16 */
-  double   theta;               /* > 0 */
+  double   theta;               /* > 0, finite */
   float    eps;                 /* >= 0 */
   const void* q;  int64_t ldq;  /* [rows][q_heads][head_dim], ld = elements from row to row */
   const void* k;  int64_t ldk;  /* [rows][kv_heads][head_dim] */
