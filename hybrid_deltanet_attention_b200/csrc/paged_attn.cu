@@ -107,7 +107,6 @@ struct Segment {
   int kvh, tile;           // kv head, row tile
   int t0, t1;              // key tiles
   int part;                // slot of the partial results, or -1
-  int flags;
 };
 
 struct Bars {
