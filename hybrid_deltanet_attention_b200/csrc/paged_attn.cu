@@ -935,7 +935,6 @@ __global__ void __launch_bounds__(kThreads_, 1)
         b->l[grp][r] = l;
         if (!(ok = pair_sync(b, quarter, meets, err))) break;
         l += b->l[grp ^ 1][r];
-        if (!(ok = pair_sync(b, quarter, meets, err))) break;
         const float inv = l > 0.f ? 1.f / l : 0.f;   // a row that saw nothing takes exact zeros
 #ifdef MK_TEST_SLOW_EPILOGUE_NS
         // a build for tests: the group that does not have the next tile reads O late
@@ -971,8 +970,8 @@ __global__ void __launch_bounds__(kThreads_, 1)
         }
         if (part >= 0 && grp == 0 && r < rows) a.ml[static_cast<long long>(part) * a.max_rows + r] = make_float2(m, l);
         // The next row tile's first product overwrites O and waits for the weights of one group only, so
-        // that group goes on once the other one has read its half too. (A barrier of its own that the MMA warp waits on
-        // was slower: ragged chunks 78 against 74 us.)
+        // that group goes on once the other one has read its half (and l) too. (A barrier of its own that the MMA warp
+        // waits on was slower: ragged chunks 78 against 74 us.)
         tc::fence_before_sync();
         if (!(ok = pair_sync(b, quarter, meets, err))) break;
       }
