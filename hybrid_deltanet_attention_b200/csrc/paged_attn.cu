@@ -22,10 +22,10 @@
 // K0 K1 V0 K2 V1 ... is the order of use, and it runs on across row tiles, so memory stays busy through
 // softmax and epilogue. Values are taken as they lie in the page (transposed by the MMA descriptor).
 //
-// Measured on a B200, per call: one token of each of 64 sequences (1.27 GB of keys and values) 203 us, 95 % of the
-// measured copy bandwidth; a 4096-token prompt (8/2 heads of 256) 66 us, 1040 TFLOP/s of causal work, where
+// Measured on several B200s, per call: one token of each of 64 sequences (1.27 GB of keys and values) 203-222 us, 87-95 %
+// of the measured copy bandwidth; a 4096-token prompt (8/2 heads of 256) 68-75 us, 920-1010 TFLOP/s of causal work, where
 // shared memory bounds a tile (128 x 128 tiles at 256 entries move 320 KB through it, 2560 clocks; measured 3400);
-// ragged chunks of 128-wide heads 70 us, bound by the chain of a group's softmax (about 3000 clocks a
+// ragged chunks of 128-wide heads 72-78 us, bound by the chain of a group's softmax (about 3000 clocks a
 // tile, two groups at work); one token over 32769 positions 25 us, of which the stream of 67 MB is half.
 #include <algorithm>
 #include <cmath>
@@ -986,7 +986,8 @@ __global__ void __launch_bounds__(kThreads_, 1)
   }
 }
 
-// Joins the partial results of the row tiles whose keys were cut: with M the largest m of the
+// Joins the partial results of the row tiles whose keys were cut (a row tile has kJoinY blocks whatever its rows, so a few rows
+// join in one round, and a full row tile over a long context in many, one after another): with M the largest m of the
 // contributors, o = sum 2^(m - M) O / sum 2^(m - M) l. blockIdx.x is the leading CTA; a task is (up to) 128 columns of
 // a row. Up to four contributors (a prompt's row tile is cut once or twice, and there are many rows) are
 // read at once by one warp, for two tasks at a time; more (a long context's few rows have one contributor

@@ -231,14 +231,14 @@ class PagedCache:
                out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Norm (where a gain is given) and rotate the queries and keys of new rows and store keys and values in
         their pages (mk_qk_norm_rope). Rows seq_start[i] .. seq_start[i+1]-1 are the last positions of sequence
-        seqs[i] (or i), whose length already counts them. Returns the bfloat16 queries."""
+        seqs[i] (or i), whose length already counts them. Returns the bfloat16 queries (rows of no sequence are not written)."""
         return _rope(self.device, q, k, v, None, q_gain, k_gain, eps, theta, rot_dim, out, None, self, layer, seq_start, seqs,
                      self._d, stream)[0]
 
     def attention(self, layer: int, q: torch.Tensor, seq_start: torch.Tensor, seqs: Optional[torch.Tensor] = None, *,
                   scale: Optional[float] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Causal attention of new rows over their sequences' pages (mk_paged_attention); q bfloat16
-        [rows][query heads][head dim], scale 1/sqrt(head dim) unless given. Returns bfloat16 like q."""
+        [rows][query heads][head dim], scale 1/sqrt(head dim) unless given. Returns bfloat16 like q (rows of no sequence are not written)."""
         index, rows, d = self._index, q.shape[0], self._d
         qp, ldq, hq = _heads(q, "q", index, _BF16, rows, d)
         start, ids, n = _new_rows(seq_start, seqs, self._n_seqs, index)

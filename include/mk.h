@@ -390,7 +390,8 @@ int mk_pages_copy(const mk_paged_cache* from, const mk_paged_cache* to, const in
  *   x = x * gain / sqrt(mean(x^2) + eps)              (per head; skipped where the gain is NULL)
  *   (x[i], x[i + rot_dim/2]) rotated by the angle position * theta^(-2i / rot_dim), i < rot_dim/2
  * (half split, as the model's attention; entries from rot_dim on are only normed). Norms and
- * rotation in fp32, angles in float64, one rounding to bf16 at the end.
+ * rotation in fp32 (a head whose squares overflow it, entries near 1e19, becomes zeros), angles in float64, one rounding
+ * to bf16 at the end.
  * With `cache`: rows seq_start[i] .. seq_start[i+1]-1 are the last
  * positions of sequence seqs[i] (or i, with seqs NULL; the sequences of a call differ), whose len already counts
  * them (see mk_pages_resize): row r has position len - seq_start[i+1] + r. Keys, and the values as they
@@ -431,6 +432,9 @@ int mk_qk_norm_rope(const mk_qk_rope* a, void* stream);
  * MK_DEVERR_BAD_PAGE and reads as zeros. The kernel's waits are bounded: one that gave up sets
  * MK_DEVERR_PIPE_TIMEOUT, and the call's results are then not valid.
  * scale: any value of magnitude at most 2e38, 0 and negative ones too; scaled scores must stay in fp32's range.
+ * Precision: scores, softmax statistics and sums are fp32. A weight enters the value product as one bf16 (off by at
+ * most 2^-8 of itself; mk_prefill's attention carries a second bf16 for the rest), the sum of weights does not, and the result
+ * is rounded to bf16 once: against float64, errors are about 1.4 times those of that last rounding alone.
  * d_q: bf16 [rows][q_heads][head_dim], d_out: bf16 likewise, ldq / ldo elements from row to
  * row (multiples of 8); 16-byte aligned. n <= 65536. q_heads a multiple of the cache's kv_heads, at most 128 times them.
  * d_scratch: at least mk_paged_attention_scratch(...) bytes, 32-byte aligned; one buffer per
